@@ -1,4 +1,5 @@
-"""Loader of libfp8bw.so (the library's C ABI, include/fp8bw.h).
+"""Loader of libfp8bw.so (the library's C ABI: include/fp8bw.h and
+include/fp8bw_layer.h).
 
 The shared library is built in-tree by build.py. There is no fallback: if it
 cannot be loaded, importing this module raises.
@@ -64,6 +65,33 @@ SIGNATURES = {
     "fp8bw_version": ([], _INT),
 }
 
+class NsJob(ctypes.Structure):
+    """fp8bw_ns_job of include/fp8bw_layer.h."""
+    _fields_ = [("g", _P), ("n", _I64), ("k", _I64), ("out", _P)]
+
+
+_F32 = ctypes.c_float
+_RMSNORM = [_P, _P, _P, _INT, _I64, _I64, _F32] + [_P] * 8
+_SWIGLU = [_P, _I64, _I64, _P, _P, _P, _P, _P]
+_SWIGLU_BWD = [_P, _P, _I64, _I64, _P, _P, _P, _P, _P]
+
+# name -> (argtypes, restype), in the order of include/fp8bw_layer.h
+LAYER_SIGNATURES = {
+    "fp8bw_rmsnorm_quantize": (_RMSNORM, _INT),
+    "fp8bw_rmsnorm_quantize_pow2": (_RMSNORM, _INT),
+    "fp8bw_rmsnorm_backward_workspace": ([_I64, _I64], _I64),
+    "fp8bw_rmsnorm_backward": ([_P, _P, _P, _P, _INT, _P, _I64, _I64, _P, _P,
+                                _P, _I64, _P], _INT),
+    "fp8bw_swiglu_quantize": (_SWIGLU, _INT),
+    "fp8bw_swiglu_quantize_pow2": (_SWIGLU, _INT),
+    "fp8bw_swiglu_backward_quantize": (_SWIGLU_BWD, _INT),
+    "fp8bw_swiglu_backward_quantize_pow2": (_SWIGLU_BWD, _INT),
+    "fp8bw_newton_schulz_workspace": ([_P, _INT], _I64),
+    "fp8bw_newton_schulz": ([_P, _INT, _INT, _INT, _F32, _F32, _F32, _F32, _P,
+                             _I64, _P], _INT),
+    "fp8bw_layer_check_device_error": ([_P], _INT),
+}
+
 LIB_PATH = _build.LIB
 _lib = None
 
@@ -77,7 +105,7 @@ def load():
         if not os.path.exists(LIB_PATH):
             raise ImportError("libfp8bw.so is missing and could not be built")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (argtypes, restype) in SIGNATURES.items():
+        for name, (argtypes, restype) in (SIGNATURES | LAYER_SIGNATURES).items():
             fn = getattr(lib, name)
             fn.argtypes = argtypes
             fn.restype = restype

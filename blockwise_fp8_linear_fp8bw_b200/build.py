@@ -1,7 +1,8 @@
 """Build the CUDA library libfp8bw.so in-tree for sm_100a (nvcc, no torch).
 
-One translation unit (csrc/api.cu includes the kernel headers); cudart is
-linked statically; the driver's TMA encoder is reached through
+Two translation units, each including its kernel headers: csrc/api.cu (the
+quantisers and GEMMs) and csrc/layer/layer.cu (the operators around them);
+cudart is linked statically; the driver's TMA encoder is reached through
 cudaGetDriverEntryPoint, so no libcuda link is needed at build time.
 """
 import os
@@ -13,19 +14,21 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8bw.so")
 ROOT = os.path.dirname(HERE)
 HEADER = os.path.join(ROOT, "include", "fp8bw.h")
+LAYER_HEADER = os.path.join(ROOT, "include", "fp8bw_layer.h")
+UNITS = [os.path.join(CSRC, "api.cu"), os.path.join(CSRC, "layer", "layer.cu")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
-    "-Xptxas", "-v",
+    "-Xptxas", "-v", "--threads", "2",
 ]
 
 
 def _sources():
-    srcs = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
-            if f.endswith((".cu", ".cuh"))]
-    return srcs + [HEADER]
+    srcs = [os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "layer"))
+            for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))]
+    return srcs + [HEADER, LAYER_HEADER]
 
 
 def _nvcc():
@@ -47,7 +50,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [_nvcc()] + NVCC_FLAGS + ["-o", tmp, os.path.join(CSRC, "api.cu")]
+    cmd = [_nvcc()] + NVCC_FLAGS + ["-o", tmp] + UNITS
     res = subprocess.run(cmd, capture_output=True, text=True)
     log = res.stdout + res.stderr
     with open(os.path.join(HERE, "build.log"), "w") as fh:

@@ -1,0 +1,809 @@
+// layer.cu -- the C ABI of the layer operators (declared in
+// include/fp8bw_layer.h): argument checks, TMA descriptors, launches. Its own
+// translation unit, with its own device error record.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "../../../include/fp8bw_layer.h"
+#include "../common.cuh"
+#include "newton_schulz.cuh"
+#include "norm.cuh"
+#include "swiglu.cuh"
+
+namespace fp8bw {
+namespace layer {
+namespace {
+
+// ---------------------------------------------------------------- device, checks
+struct Device {
+  int ordinal = 0;
+  int sm_count = 0;
+};
+
+int current_device(Device* out) {
+  struct Info {
+    int checked = 0;   // 0 = unknown, 1 = sm_100, -1 = other
+    int sms = 0;
+  };
+  static Info info[kMaxDevices];
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return FP8BW_ERR_DEVICE;
+  // makes the primary context current on this thread (the tensor-map encoder
+  // needs one)
+  if (cudaSetDevice(dev) != cudaSuccess) return FP8BW_ERR_DEVICE;
+  std::lock_guard<std::mutex> lock(mu);
+  Info& d = info[dev];
+  if (d.checked == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return FP8BW_ERR_DEVICE;
+    d.checked = (major == 10 && minor == 0) ? 1 : -1;
+  }
+  if (d.checked != 1) return FP8BW_ERR_DEVICE;
+  out->ordinal = dev;
+  out->sm_count = d.sms;
+  return FP8BW_OK;
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxNormCols = 32768;    // a row fits 512 threads x 8 chunks
+constexpr int64_t kMaxGluCols = int64_t(1) << 22;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t pad16(int64_t rows) { return (rows + 15) / 16 * 16; }
+bool cols_ok(int64_t c, int64_t most) { return c >= 0 && c % 16 == 0 && c <= most; }
+
+// The buffers of a call: each is checked for presence and alignment, and
+// every output against every other buffer.
+struct Buffers {
+  struct Item {
+    uintptr_t lo, hi;
+    bool out;
+  };
+  Item item[32];
+  int n = 0;
+  int status = FP8BW_OK;
+  void add(const void* p, int64_t bytes, bool required, bool out) {
+    if (status != FP8BW_OK) return;
+    if (p == nullptr) {
+      if (required && bytes > 0) status = FP8BW_ERR_NULL;
+      return;
+    }
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (a % 16 != 0) {
+      status = FP8BW_ERR_ALIGN;
+      return;
+    }
+    if (bytes <= 0) return;
+    if (n == static_cast<int>(sizeof item / sizeof item[0])) {
+      status = FP8BW_ERR_SHAPE;
+      return;
+    }
+    item[n++] = Item{a, a + static_cast<uintptr_t>(bytes), out};
+  }
+  void in(const void* p, int64_t bytes, bool required = true) { add(p, bytes, required, false); }
+  void out(const void* p, int64_t bytes, bool required = true) { add(p, bytes, required, true); }
+  int check() const {
+    if (status != FP8BW_OK) return status;
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j)
+        if ((item[i].out || item[j].out) && item[i].lo < item[j].hi && item[j].lo < item[i].hi)
+          return FP8BW_ERR_ALIAS;
+    return FP8BW_OK;
+  }
+};
+
+int launched(cudaError_t e) {
+  if (e != cudaSuccess) return FP8BW_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? FP8BW_OK : FP8BW_ERR_LAUNCH;
+}
+
+// ---------------------------------------------------------------- tensor maps
+int encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
+              uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+              CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (encode == nullptr) {
+      void* p = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+              cudaSuccess ||
+          q != cudaDriverEntryPointSuccess || p == nullptr)
+        return FP8BW_ERR_CUDA;
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+  }
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FP8BW_OK
+             : FP8BW_ERR_CUDA;
+}
+
+// bf16 [rows, cols] with rows of row_bytes, read in 128 x 128 tiles.
+int encode_tiles(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                 int64_t row_bytes) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, static_cast<uint64_t>(cols),
+                   static_cast<uint64_t>(rows), static_cast<uint64_t>(row_bytes), kTile, kTile,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+template <typename K>
+int allow_smem(DevicePrep& prep, int dev, K kernel, int bytes) {
+  int unused = 0;
+  return prepare_for_device(prep, dev, &unused, [&](int*) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+                   cudaSuccess
+               ? static_cast<int>(FP8BW_OK)
+               : static_cast<int>(FP8BW_ERR_LAUNCH);
+  });
+}
+
+// ---------------------------------------------------------------- norm
+int threads_per_row(int64_t chunks, int v) { return static_cast<int>(cdiv(cdiv(chunks, v), 32) * 32); }
+
+template <int V, bool POW2>
+int launch_norm_rows(NormArgs a, cudaStream_t stream) {
+  a.tpr = threads_per_row(a.cols / 8, V);
+  const int groups = std::max(1, 256 / a.tpr);
+  const int64_t blocks = cdiv(a.row_end - a.row0, groups);
+  return launched(launch_kernel(rmsnorm_row_kernel<V, POW2>, dim3(static_cast<unsigned>(blocks)),
+                                dim3(groups * a.tpr), 0, stream, a));
+}
+
+template <bool POW2>
+int norm_rows(const NormArgs& a, const Device& dev, cudaStream_t stream) {
+  const int64_t chunks = a.cols / 8;
+  // Many rows: one warp per row where its registers suffice (no block barrier,
+  // all of a row's loads in flight at once). Few rows: the most threads per
+  // row, for latency.
+  const bool many = a.row_end - a.row0 > 4 * static_cast<int64_t>(dev.sm_count);
+  const int64_t per = many ? 32 : 1024;
+  if (chunks <= per) return launch_norm_rows<1, POW2>(a, stream);
+  if (many && chunks <= 2 * per) return launch_norm_rows<2, POW2>(a, stream);
+  if (chunks <= (many ? 4 * per : 2 * per)) return launch_norm_rows<4, POW2>(a, stream);
+  return launch_norm_rows<8, POW2>(a, stream);
+}
+
+// Rows whose h stays in L2 until the column pass reads it (half of its 126 MB).
+constexpr int64_t kNormChunkBytes = int64_t(64) << 20;
+
+template <bool POW2>
+int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* gamma,
+                     int gamma_is_f32, int64_t rows, int64_t cols, float eps, uint16_t* h,
+                     float* rstd, uint16_t* y, uint8_t* q, float* s, uint8_t* q_t, float* s_t,
+                     void* stream) {
+  if (rows < 0 || rows > kMaxRows || !cols_ok(cols, kMaxNormCols)) return FP8BW_ERR_SHAPE;
+  if (!(eps >= 0.0f)) return FP8BW_ERR_SHAPE;
+  const int64_t rp = pad16(rows), n = rows * cols;
+  if (n > 0 && ((q == nullptr) != (s == nullptr) || (q_t == nullptr) != (s_t == nullptr)))
+    return FP8BW_ERR_NULL;
+  if (n > 0 && residual == nullptr && h != nullptr) return FP8BW_ERR_NULL;
+  Buffers b;
+  b.in(x, 2 * n);
+  b.in(residual, 2 * n, false);
+  b.in(gamma, cols * (gamma_is_f32 ? 4 : 2));
+  b.out(h, 2 * n, residual != nullptr);
+  b.out(rstd, 4 * rows, q_t != nullptr);
+  b.out(y, 2 * n, false);
+  b.out(q, rp * cols, false);
+  b.out(s, 4 * cdiv(cols, 128) * rp, false);
+  b.out(q_t, rp * cols, false);
+  b.out(s_t, 4 * cdiv(rp, 128) * cols, false);
+  int st = b.check();
+  if (st != FP8BW_OK) return st;
+  Device dev;
+  st = current_device(&dev);
+  if (st != FP8BW_OK || n == 0) return st;
+
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.gamma_f32 = gamma_is_f32 != 0;
+  a.rows = rows;
+  a.rows_pad = rp;
+  a.cols = cols;
+  a.eps = eps;
+  a.h = h;
+  a.rstd = rstd;
+  a.y = y;
+  a.q = q;
+  a.s = s;
+  if (q_t == nullptr) {
+    a.row0 = 0;
+    a.row_end = rp;
+    return norm_rows<POW2>(a, dev, cs);
+  }
+  CUtensorMap map;
+  st = encode_tiles(&map, residual != nullptr ? h : x, rows, cols, 2 * cols);
+  if (st != FP8BW_OK) return st;
+  static DevicePrep prep;
+  st = allow_smem(prep, dev.ordinal, norm_col_kernel<POW2>, NormColSmem::kAlloc);
+  if (st != FP8BW_OK) return st;
+  const int64_t chunk = std::max<int64_t>(128, kNormChunkBytes / (2 * cols) / 128 * 128);
+  for (int64_t r0 = 0; r0 < rp; r0 += chunk) {
+    a.row0 = r0;
+    a.row_end = std::min(rp, r0 + chunk);
+    st = norm_rows<POW2>(a, dev, cs);
+    if (st != FP8BW_OK) return st;
+    NormColArgs c{};
+    c.rstd = rstd;
+    c.gamma = gamma;
+    c.gamma_f32 = a.gamma_f32;
+    c.rows = rows;
+    c.rows_pad = rp;
+    c.cols = cols;
+    c.tr0 = static_cast<int>(r0 / 128);
+    c.tiles_r = static_cast<int>(cdiv(a.row_end - r0, 128));
+    c.tiles_c = static_cast<int>(cdiv(cols, 128));
+    c.q_t = q_t;
+    c.s_t = s_t;
+    const int tiles = c.tiles_r * c.tiles_c;
+    st = launched(launch_kernel(norm_col_kernel<POW2>, dim3(std::min(tiles, 2 * dev.sm_count)),
+                                dim3(kTileThreads), NormColSmem::kAlloc, cs, map, c));
+    if (st != FP8BW_OK) return st;
+  }
+  return FP8BW_OK;
+}
+
+// ---------------------------------------------------------------- norm, backward
+constexpr int64_t kBwdMaxBlocks = 296;    // two per SM of 148
+
+struct BwdPlan {
+  int v, r, tpr, groups;
+  int64_t blocks, parts;
+};
+
+// The fewest chunks per thread that fit a row into 512 threads; four rows (or
+// four chunks) per thread and iteration, to have the loads in flight.
+BwdPlan bwd_plan(int64_t rows, int64_t cols) {
+  BwdPlan p;
+  const int64_t chunks = cols / 8;
+  p.v = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+  p.r = p.v >= 4 ? 1 : 4 / p.v;
+  p.tpr = threads_per_row(chunks, p.v);
+  p.groups = std::max(1, 256 / std::max(p.tpr, 1));
+  p.blocks = std::min<int64_t>(kBwdMaxBlocks, cdiv(rows, static_cast<int64_t>(p.groups) * p.r));
+  p.parts = p.blocks * p.groups;
+  return p;
+}
+
+int rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd, const void* gamma,
+                     int gamma_is_f32, const uint16_t* dres, int64_t rows, int64_t cols,
+                     uint16_t* dh, float* dgamma, void* ws, int64_t ws_bytes, void* stream) {
+  if (rows < 0 || rows > kMaxRows || !cols_ok(cols, kMaxNormCols)) return FP8BW_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  const int64_t need = n > 0 ? bwd_plan(rows, cols).parts * cols * 4 : 0;
+  if (ws_bytes < need) return FP8BW_ERR_SHAPE;
+  Buffers b;
+  b.in(dy, 2 * n);
+  b.in(h, 2 * n);
+  b.in(rstd, 4 * rows);
+  b.in(gamma, cols * (gamma_is_f32 ? 4 : 2), n > 0);
+  b.in(dres, 2 * n, false);
+  b.out(dh, 2 * n);
+  b.out(dgamma, 4 * cols);
+  b.out(ws, need);
+  int st = b.check();
+  if (st != FP8BW_OK) return st;
+  Device dev;
+  st = current_device(&dev);
+  if (st != FP8BW_OK || cols == 0) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (rows == 0)      // a sum over no rows
+    return cudaMemsetAsync(dgamma, 0, static_cast<size_t>(cols) * 4, cs) == cudaSuccess
+               ? FP8BW_OK
+               : FP8BW_ERR_CUDA;
+  const BwdPlan p = bwd_plan(rows, cols);
+  NormBwdArgs a{dy, h, rstd, gamma, gamma_is_f32 != 0, dres, rows, cols, dh,
+                static_cast<float*>(ws), p.tpr};
+  using Kernel = void (*)(NormBwdArgs);
+  const Kernel kernel = p.v == 1   ? rmsnorm_bwd_kernel<1, 4>
+                        : p.v == 2 ? rmsnorm_bwd_kernel<2, 2>
+                        : p.v == 4 ? rmsnorm_bwd_kernel<4, 1>
+                                   : rmsnorm_bwd_kernel<8, 1>;
+  st = launched(launch_kernel(kernel, dim3(static_cast<unsigned>(p.blocks)),
+                              dim3(p.groups * p.tpr), 0, cs, a));
+  if (st != FP8BW_OK) return st;
+  return launched(launch_kernel(dgamma_reduce_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32))),
+                                dim3(1024), 0, cs, static_cast<const float*>(ws), p.parts, cols,
+                                dgamma));
+}
+
+// ---------------------------------------------------------------- gated product
+bool glu_shape_ok(int64_t rows, int64_t f) {
+  return rows >= 0 && rows <= kMaxRows && cols_ok(f, kMaxGluCols) &&
+         cdiv(rows, 128) * cdiv(2 * f, 128) <= INT32_MAX;
+}
+
+template <bool POW2>
+int swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, float* s,
+                    uint8_t* q_t, float* s_t, void* stream) {
+  if (!glu_shape_ok(rows, f)) return FP8BW_ERR_SHAPE;
+  const int64_t rp = pad16(rows), n = rows * f;
+  if (n > 0 && (q_t == nullptr) != (s_t == nullptr)) return FP8BW_ERR_NULL;
+  Buffers b;
+  b.in(gu, 4 * n);
+  b.out(q, rp * f);
+  b.out(s, 4 * cdiv(f, 128) * rp);
+  b.out(q_t, rp * f, false);
+  b.out(s_t, 4 * cdiv(rp, 128) * f, false);
+  int st = b.check();
+  if (st != FP8BW_OK) return st;
+  Device dev;
+  st = current_device(&dev);
+  if (st != FP8BW_OK || n == 0) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (q_t == nullptr) {
+    const GluRowArgs a{gu, rows, rp, f, q, s};
+    return launched(launch_kernel(swiglu_row_kernel<POW2>,
+                                  dim3(static_cast<unsigned>(rp / 16),
+                                       static_cast<unsigned>(cdiv(f, 128))),
+                                  dim3(kGluRowThreads), 0, cs, a));
+  }
+  CUtensorMap mg, mu;
+  st = encode_tiles(&mg, gu, rows, f, 4 * f);
+  if (st == FP8BW_OK) st = encode_tiles(&mu, gu + f, rows, f, 4 * f);
+  if (st != FP8BW_OK) return st;
+  static DevicePrep prep;
+  st = allow_smem(prep, dev.ordinal, swiglu_tile_kernel<POW2>, GluFwdSmem::kAlloc);
+  if (st != FP8BW_OK) return st;
+  const GluTileArgs a{rp, f, static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
+                      q, s, q_t, s_t};
+  const int tiles = a.tiles_r * a.tiles_c;
+  return launched(launch_kernel(swiglu_tile_kernel<POW2>, dim3(std::min(tiles, 2 * dev.sm_count)),
+                                dim3(kTileThreads), GluFwdSmem::kAlloc, cs, mg, mu, a));
+}
+
+template <bool POW2>
+int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t rows, int64_t f,
+                             uint8_t* q, float* s, uint8_t* q_t, float* s_t, void* stream) {
+  if (!glu_shape_ok(rows, f)) return FP8BW_ERR_SHAPE;
+  const int64_t rp = pad16(rows), n = rows * f;
+  Buffers b;
+  b.in(da, 2 * n);
+  b.in(gu, 4 * n);
+  b.out(q, 2 * rp * f);
+  b.out(s, 4 * cdiv(2 * f, 128) * rp);
+  b.out(q_t, 2 * rp * f);
+  b.out(s_t, 4 * cdiv(rp, 128) * 2 * f);
+  int st = b.check();
+  if (st != FP8BW_OK) return st;
+  Device dev;
+  st = current_device(&dev);
+  if (st != FP8BW_OK || n == 0) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  GluTileArgs a{rp, f, static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
+                q, s, q_t, s_t};
+  if (f % 128 != 0) {
+    a.tiles_c = static_cast<int>(cdiv(2 * f, 128));
+    const GluRaggedArgs r{gu, da, rows, a};
+    const int tiles = a.tiles_r * a.tiles_c;
+    return launched(launch_kernel(swiglu_bwd_ragged_kernel<POW2>,
+                                  dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kTileThreads),
+                                  TileEmit::kBytes + 128, cs, r));
+  }
+  CUtensorMap mg, mu, md;
+  st = encode_tiles(&mg, gu, rows, f, 4 * f);
+  if (st == FP8BW_OK) st = encode_tiles(&mu, gu + f, rows, f, 4 * f);
+  if (st == FP8BW_OK) st = encode_tiles(&md, da, rows, f, 2 * f);
+  if (st != FP8BW_OK) return st;
+  static DevicePrep prep;
+  st = allow_smem(prep, dev.ordinal, swiglu_bwd_tile_kernel<POW2>, GluBwdSmem::kAlloc);
+  if (st != FP8BW_OK) return st;
+  const int tiles = a.tiles_r * a.tiles_c;
+  return launched(launch_kernel(swiglu_bwd_tile_kernel<POW2>,
+                                dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kTileThreads),
+                                GluBwdSmem::kAlloc, cs, mg, mu, md, a));
+}
+
+// ---------------------------------------------------------------- Newton-Schulz
+constexpr int kMaxSteps = 64;
+constexpr int64_t kMaxNsDim = int64_t(1) << 17;
+
+struct NsBuffers {
+  uint16_t* hi[2];
+  uint16_t* lo;
+  uint16_t* a;
+  uint16_t* b;
+  double* part;
+};
+
+int64_t ns_align(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+int64_t ns_job_bytes(int64_t n, int64_t k) {
+  if (n == 0 || k == 0) return 0;
+  const int64_t r = std::min(n, k);
+  return 3 * ns_align(2 * n * k) + 2 * ns_align(2 * r * r) + ns_align(8 * ns::kNormBlocks);
+}
+
+NsBuffers ns_carve(uint8_t* p, int64_t n, int64_t k) {
+  const int64_t r = std::min(n, k);
+  const int64_t x = ns_align(2 * n * k), m = ns_align(2 * r * r);
+  NsBuffers b;
+  b.hi[0] = reinterpret_cast<uint16_t*>(p);
+  b.hi[1] = reinterpret_cast<uint16_t*>(p + x);
+  b.lo = reinterpret_cast<uint16_t*>(p + 2 * x);
+  b.a = reinterpret_cast<uint16_t*>(p + 3 * x);
+  b.b = reinterpret_cast<uint16_t*>(p + 3 * x + m);
+  b.part = reinterpret_cast<double*>(p + 3 * x + 2 * m);
+  return b;
+}
+
+bool ns_dims_ok(int64_t n, int64_t k) {
+  return n >= 0 && k >= 0 && n % 16 == 0 && k % 16 == 0 && n <= kMaxNsDim && k <= kMaxNsDim;
+}
+
+// One GEMM over all jobs: an operand is a 16-bit matrix with `rows` rows of
+// `cols` contiguous elements, read K-major (contraction along the row) or
+// MN-major.
+struct NsOperand {
+  const uint16_t* p;
+  int64_t rows, cols;
+  bool mn;
+};
+struct NsGemm {
+  NsOperand a, b;
+  const uint16_t* c;      // poly: A; update, last: the old hi
+  const uint16_t* lo;
+  uint16_t* out;
+  int64_t rows, cols, kc;
+};
+
+int64_t ns_tiles(const NsGemm& g, int bn, bool sym) {
+  const int64_t tm = cdiv(g.rows, 256), tn = cdiv(g.cols, bn);
+  if (!sym) return tm * tn;
+  const int64_t per = 256 / bn;
+  return tm * tn - per * (tm * (tm - 1) / 2);
+}
+
+// The longest cluster's work under the kernel's tile order, in 256-column
+// chunk units (a tile also costs about two chunks of pipeline fill).
+double ns_makespan(const NsGemm* g, int count, int bn, bool sym, int clusters) {
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) total += ns_tiles(g[i], bn, sym);
+  const int64_t waves = cdiv(total, clusters);
+  if (waves > 16) {      // long: the sum decides
+    double sum = 0.0;
+    for (int i = 0; i < count; ++i)
+      sum += static_cast<double>(ns_tiles(g[i], bn, sym)) * (cdiv(g[i].kc, ns::BK) + 2) * bn;
+    return sum / 256.0 / clusters;
+  }
+  auto cost_of = [&](int64_t t) {
+    int i = 0;
+    while (t >= ns_tiles(g[i], bn, sym)) t -= ns_tiles(g[i++], bn, sym);
+    return static_cast<double>(cdiv(g[i].kc, ns::BK) + 2) * bn / 256.0;
+  };
+  double worst = 0.0;
+  for (int c = 0; c < clusters; ++c) {
+    double w = 0.0;
+    for (int64_t k = 0; k < waves; ++k) {
+      const int64_t t = k * clusters + ((k & 1) ? clusters - 1 - c : c);
+      if (t < total) w += cost_of(t);
+    }
+    worst = std::max(worst, w);
+  }
+  return worst;
+}
+
+int encode_operand(CUtensorMap* map, const NsOperand& o, int rows) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, o.p, static_cast<uint64_t>(o.cols),
+                   static_cast<uint64_t>(o.rows), static_cast<uint64_t>(2 * o.cols), 64,
+                   o.mn ? 64 : rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+int encode_boxes(CUtensorMap* map, const void* p, int64_t rows, int64_t cols) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, p, static_cast<uint64_t>(cols),
+                   static_cast<uint64_t>(rows), static_cast<uint64_t>(2 * cols), 32, 32,
+                   CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+// Everything a launch of one phase needs, prepared once per call.
+struct NsLaunch {
+  ns::Maps maps;
+  ns::Args args;
+  int bn = 256;
+  int clusters = 0;
+};
+
+template <int BN, int MODE>
+int ns_clusters(const Device& dev, int* clusters) {
+  static DevicePrep prep;
+  auto kernel = ns::ns_gemm_kernel<BN, MODE>;
+  return prepare_for_device(prep, dev.ordinal, clusters, [&](int* out) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ns::Layout<BN>::kAlloc) != cudaSuccess)
+      return static_cast<int>(FP8BW_ERR_LAUNCH);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * dev.sm_count);
+    cfg.blockDim = dim3(ns::kThreads);
+    cfg.dynamicSmemBytes = ns::Layout<BN>::kAlloc;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(out, kernel, &cfg) == cudaSuccess && *out >= 1
+               ? static_cast<int>(FP8BW_OK)
+               : static_cast<int>(FP8BW_ERR_LAUNCH);
+  });
+}
+
+template <int MODE>
+int ns_prepare(NsLaunch* l, const NsGemm* in, int count, const Device& dev) {
+  constexpr bool kSym = MODE == ns::kGram || MODE == ns::kPoly;
+  NsGemm g[ns::kMaxJobs];
+  std::copy(in, in + count, g);
+  // long contractions first (see the kernel's tile order)
+  std::stable_sort(g, g + count, [](const NsGemm& x, const NsGemm& y) { return x.kc > y.kc; });
+  int c256 = 0, c128 = 0;
+  int st = ns_clusters<256, MODE>(dev, &c256);
+  if (st == FP8BW_OK) st = ns_clusters<128, MODE>(dev, &c128);
+  if (st != FP8BW_OK) return st;
+  // 128-wide tiles where they spread the work better over the clusters
+  l->bn = ns_makespan(g, count, 128, kSym, c128) < 0.95 * ns_makespan(g, count, 256, kSym, c256)
+              ? 128
+              : 256;
+  l->clusters = l->bn == 256 ? c256 : c128;
+  std::memset(&l->args, 0, sizeof l->args);
+  std::memset(&l->maps, 0, sizeof l->maps);
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i) {
+    ns::Job& j = l->args.job[i];
+    j.rows = static_cast<int>(g[i].rows);
+    j.cols = static_cast<int>(g[i].cols);
+    j.tiles_m = static_cast<int>(cdiv(g[i].rows, 256));
+    j.tiles_n = static_cast<int>(cdiv(g[i].cols, l->bn));
+    j.chunks = static_cast<int>(cdiv(g[i].kc, ns::BK));
+    j.a_mn = g[i].a.mn;
+    j.b_mn = g[i].b.mn;
+    tiles += ns_tiles(g[i], l->bn, kSym);
+    if (tiles > INT32_MAX / 2) return FP8BW_ERR_SHAPE;
+    j.tile_end = static_cast<int>(tiles);
+    st = encode_operand(&l->maps.a[i], g[i].a, ns::BM);
+    if (st == FP8BW_OK) st = encode_operand(&l->maps.b[i], g[i].b, l->bn / 2);
+    if (st == FP8BW_OK && MODE != ns::kGram)
+      st = encode_boxes(&l->maps.c[i], g[i].c, g[i].rows, g[i].cols);
+    if (st == FP8BW_OK && !kSym) st = encode_boxes(&l->maps.lo[i], g[i].lo, g[i].rows, g[i].cols);
+    if (st == FP8BW_OK) st = encode_boxes(&l->maps.out[i], g[i].out, g[i].rows, g[i].cols);
+    if (st != FP8BW_OK) return st;
+  }
+  l->args.count = count;
+  l->clusters = static_cast<int>(std::min<int64_t>(l->clusters, tiles));
+  return FP8BW_OK;
+}
+
+template <int MODE>
+int ns_launch(const NsLaunch& l, cudaStream_t stream) {
+  const dim3 grid(2 * l.clusters), block(ns::kThreads);
+  if (l.bn == 256)
+    return launched(launch_kernel(ns::ns_gemm_kernel<256, MODE>, grid, block,
+                                  ns::Layout<256>::kAlloc, stream, l.maps, l.args));
+  return launched(launch_kernel(ns::ns_gemm_kernel<128, MODE>, grid, block,
+                                ns::Layout<128>::kAlloc, stream, l.maps, l.args));
+}
+
+int newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, float ca, float cb,
+                  float cc, float eps, void* ws, int64_t ws_bytes, void* stream) {
+  if (count < 0 || count > ns::kMaxJobs || steps < 1 || steps > kMaxSteps || !(eps >= 0.0f) ||
+      !std::isfinite(ca) || !std::isfinite(cb) || !std::isfinite(cc))
+    return FP8BW_ERR_SHAPE;
+  if (count > 0 && jobs == nullptr) return FP8BW_ERR_NULL;
+  Buffers b;
+  int64_t need = 0;
+  for (int i = 0; i < count; ++i) {
+    const fp8bw_ns_job& j = jobs[i];
+    if (!ns_dims_ok(j.n, j.k)) return FP8BW_ERR_SHAPE;
+    b.in(j.g, j.n * j.k * (g_is_f32 ? 4 : 2));
+    b.out(j.out, 2 * j.n * j.k);
+    need += ns_job_bytes(j.n, j.k);
+  }
+  if (ws_bytes < need) return FP8BW_ERR_SHAPE;
+  b.out(ws, need);
+  int st = b.check();
+  if (st != FP8BW_OK) return st;
+  if (reinterpret_cast<uintptr_t>(ws) % 128 != 0) return FP8BW_ERR_ALIGN;
+  Device dev;
+  st = current_device(&dev);
+  if (st != FP8BW_OK) return st;
+
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  fp8bw_ns_job live[ns::kMaxJobs];
+  NsBuffers buf[ns::kMaxJobs];
+  ns::InArgs in{};
+  in.g_f32 = g_is_f32 != 0;
+  in.eps = eps;
+  int nl = 0;
+  int64_t most = 0;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  for (int i = 0; i < count; ++i) {
+    const fp8bw_ns_job& j = jobs[i];
+    if (j.n == 0 || j.k == 0) continue;
+    live[nl] = j;
+    buf[nl] = ns_carve(p, j.n, j.k);
+    p += ns_job_bytes(j.n, j.k);
+    in.job[nl] = ns::InJob{j.g, j.n * j.k, buf[nl].part, buf[nl].hi[0], buf[nl].lo};
+    most = std::max(most, j.n * j.k);
+    ++nl;
+  }
+  if (nl == 0) return FP8BW_OK;
+
+  // the phases' launches: the iterate alternates between hi[0] and hi[1]
+  NsLaunch gram[2], poly, update[2], last;
+  for (int parity = 0; parity < 2; ++parity) {
+    NsGemm gg[ns::kMaxJobs], gu[ns::kMaxJobs], gl[ns::kMaxJobs];
+    for (int i = 0; i < nl; ++i) {
+      const int64_t n = live[i].n, k = live[i].k, r = std::min(n, k), c = std::max(n, k);
+      const bool tall = n > k;
+      const NsBuffers& w = buf[i];
+      const uint16_t* x = w.hi[parity];
+      gg[i] = NsGemm{{x, n, k, tall}, {x, n, k, tall}, nullptr, nullptr, w.a, r, r, c};
+      const NsOperand m{w.b, r, r, false};
+      if (tall)
+        gu[i] = NsGemm{{x, n, k, false}, m, x, w.lo, w.hi[1 - parity], n, k, r};
+      else
+        gu[i] = NsGemm{m, {x, n, k, true}, x, w.lo, w.hi[1 - parity], n, k, r};
+      gl[i] = gu[i];
+      gl[i].out = live[i].out;
+    }
+    if (parity < steps) {
+      st = ns_prepare<ns::kGram>(&gram[parity], gg, nl, dev);
+      if (st != FP8BW_OK) return st;
+      gram[parity].args.alpha = ns::kAScale / (ns::kXScale * ns::kXScale);
+    }
+    if (parity < steps - 1) {
+      st = ns_prepare<ns::kUpdate>(&update[parity], gu, nl, dev);
+      if (st != FP8BW_OK) return st;
+      update[parity].args.alpha = 1.0f / ns::kAScale;
+    }
+    if (parity == ((steps - 1) & 1)) {
+      st = ns_prepare<ns::kLast>(&last, gl, nl, dev);
+      if (st != FP8BW_OK) return st;
+      last.args.alpha = 1.0f / (ns::kAScale * ns::kXScale);
+    }
+  }
+  {
+    NsGemm gp[ns::kMaxJobs];
+    for (int i = 0; i < nl; ++i) {
+      const int64_t r = std::min(live[i].n, live[i].k);
+      const NsOperand m{buf[i].a, r, r, false};
+      gp[i] = NsGemm{m, m, buf[i].a, nullptr, buf[i].b, r, r, r};
+    }
+    st = ns_prepare<ns::kPoly>(&poly, gp, nl, dev);
+    if (st != FP8BW_OK) return st;
+    poly.args.alpha = cc / ns::kAScale;
+    poly.args.beta = cb;
+  }
+
+  st = launched(launch_kernel(ns::ns_sumsq_kernel, dim3(ns::kNormBlocks, nl),
+                              dim3(ns::kSplitThreads), 0, cs, in));
+  if (st != FP8BW_OK) return st;
+  const int64_t blocks = std::min<int64_t>(cdiv(most, 8 * ns::kSplitThreads), 8 * dev.sm_count / nl);
+  st = launched(launch_kernel(ns::ns_split_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, blocks)), nl),
+                              dim3(ns::kSplitThreads), 0, cs, in));
+  for (int i = 0; st == FP8BW_OK && i < steps; ++i) {
+    const float shift = i >= ns::kShiftStep ? cb + cc : 0.0f;
+    poly.args.diag = shift * ns::kAScale;
+    update[i & 1].args.beta = ca + shift;
+    last.args.beta = (ca + shift) / ns::kXScale;
+    st = ns_launch<ns::kGram>(gram[i & 1], cs);
+    if (st == FP8BW_OK) st = ns_launch<ns::kPoly>(poly, cs);
+    if (st != FP8BW_OK) break;
+    st = i + 1 < steps ? ns_launch<ns::kUpdate>(update[i & 1], cs) : ns_launch<ns::kLast>(last, cs);
+  }
+  return st;
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace fp8bw
+
+using namespace fp8bw;
+
+extern "C" {
+
+int fp8bw_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* gamma,
+                           int gamma_is_f32, int64_t rows, int64_t cols, float eps, uint16_t* h,
+                           float* rstd, uint16_t* y, uint8_t* q, float* s, uint8_t* q_t,
+                           float* s_t, void* stream) {
+  return layer::rmsnorm_quantize<false>(x, residual, gamma, gamma_is_f32, rows, cols, eps, h, rstd,
+                                        y, q, s, q_t, s_t, stream);
+}
+
+int fp8bw_rmsnorm_quantize_pow2(const uint16_t* x, const uint16_t* residual, const void* gamma,
+                                int gamma_is_f32, int64_t rows, int64_t cols, float eps,
+                                uint16_t* h, float* rstd, uint16_t* y, uint8_t* q, float* s,
+                                uint8_t* q_t, float* s_t, void* stream) {
+  return layer::rmsnorm_quantize<true>(x, residual, gamma, gamma_is_f32, rows, cols, eps, h, rstd,
+                                       y, q, s, q_t, s_t, stream);
+}
+
+int64_t fp8bw_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > layer::kMaxRows || !layer::cols_ok(cols, layer::kMaxNormCols))
+    return FP8BW_ERR_SHAPE;
+  return rows * cols > 0 ? layer::bwd_plan(rows, cols).parts * cols * 4 : 0;
+}
+
+int fp8bw_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd,
+                           const void* gamma, int gamma_is_f32, const uint16_t* dres, int64_t rows,
+                           int64_t cols, uint16_t* dh, float* dgamma, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  return layer::rmsnorm_backward(dy, h, rstd, gamma, gamma_is_f32, dres, rows, cols, dh, dgamma,
+                                 workspace, workspace_bytes, stream);
+}
+
+int fp8bw_swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, float* s,
+                          uint8_t* q_t, float* s_t, void* stream) {
+  return layer::swiglu_quantize<false>(gu, rows, f, q, s, q_t, s_t, stream);
+}
+
+int fp8bw_swiglu_quantize_pow2(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, float* s,
+                               uint8_t* q_t, float* s_t, void* stream) {
+  return layer::swiglu_quantize<true>(gu, rows, f, q, s, q_t, s_t, stream);
+}
+
+int fp8bw_swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t rows, int64_t f,
+                                   uint8_t* q, float* s, uint8_t* q_t, float* s_t, void* stream) {
+  return layer::swiglu_backward_quantize<false>(da, gu, rows, f, q, s, q_t, s_t, stream);
+}
+
+int fp8bw_swiglu_backward_quantize_pow2(const uint16_t* da, const uint16_t* gu, int64_t rows,
+                                        int64_t f, uint8_t* q, float* s, uint8_t* q_t, float* s_t,
+                                        void* stream) {
+  return layer::swiglu_backward_quantize<true>(da, gu, rows, f, q, s, q_t, s_t, stream);
+}
+
+int64_t fp8bw_newton_schulz_workspace(const fp8bw_ns_job* jobs, int count) {
+  if (count < 0 || count > ns::kMaxJobs) return FP8BW_ERR_SHAPE;
+  if (count > 0 && jobs == nullptr) return FP8BW_ERR_NULL;
+  int64_t need = 0;
+  for (int i = 0; i < count; ++i) {
+    if (!layer::ns_dims_ok(jobs[i].n, jobs[i].k)) return FP8BW_ERR_SHAPE;
+    need += layer::ns_job_bytes(jobs[i].n, jobs[i].k);
+  }
+  return need;
+}
+
+int fp8bw_newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, float a,
+                        float b, float c, float eps, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  return layer::newton_schulz(jobs, count, g_is_f32, steps, a, b, c, eps, workspace,
+                              workspace_bytes, stream);
+}
+
+int fp8bw_layer_check_device_error(void* stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return FP8BW_ERR_CUDA;
+  uint32_t v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, fp8bw::g_device_error, sizeof v) != cudaSuccess)
+    return FP8BW_ERR_CUDA;
+  if (v == 0u) return FP8BW_OK;
+  if (cudaMemcpyToSymbol(fp8bw::g_device_error, &zero, sizeof zero) != cudaSuccess)
+    return FP8BW_ERR_CUDA;
+  return FP8BW_ERR_DEVICE_TIMEOUT;
+}
+
+}  // extern "C"

@@ -5,7 +5,9 @@ current CUDA stream -> cudaStream_t); every step of the computation runs in
 the CUDA library. The `fp8bw_*` functions take pre-allocated outputs; the
 short-named helpers allocate the outputs with torch and call them.
 """
+import contextlib
 import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -361,10 +363,303 @@ def fp8bw_check_device_error(stream=None, device=None):
     """Synchronise `stream` and raise Fp8bwError if a kernel of the library on
     that device (`device`, else the stream's, else the current one) recorded
     an expired wait or a bad power-of-two scale since the last check."""
-    _device_call("fp8bw_check_device_error", stream, device)
+    # the layer operators keep a record of their own: both are read and cleared
+    try:
+        _device_call("fp8bw_layer_check_device_error", stream, device)
+    finally:
+        _device_call("fp8bw_check_device_error", stream, device)
+
+
+# ----------------------------------------------------------- layer operators
+# (include/fp8bw_layer.h)
+
+_NS_COEFFS = (3.4445, -4.7750, 2.0315)
+_NS_MAX_JOBS = 8
+
+
+def _pad16(rows):
+    return (rows + 15) // 16 * 16
+
+
+def _gamma_is_f32(gamma, cols):
+    if gamma.dtype not in (torch.bfloat16, torch.float32) or \
+            tuple(gamma.shape) != (cols,):
+        raise ValueError("gamma: expected bf16 or fp32 (%d,), got %s %s"
+                         % (cols, gamma.dtype, tuple(gamma.shape)))
+    return 1 if gamma.dtype == torch.float32 else 0
+
+
+def _expect_2d(t, dtype, name):
+    if t.dtype != dtype or len(t.shape) != 2:
+        raise ValueError("%s: expected a 2-D %s tensor, got %s %s"
+                         % (name, dtype, t.dtype, tuple(t.shape)))
+
+
+def _expect_codes(q, s, q_t, s_t, rows, cols):
+    """Codes of a [rows, cols] tensor: rows padded to a multiple of 16."""
+    rp = _pad16(rows)
+    for name, t, dtype, shape in (
+            ("q", q, torch.uint8, (rp, cols)),
+            ("s", s, torch.float32, (_cdiv(cols, 128), rp)),
+            ("q_t", q_t, torch.uint8, (cols, rp)),
+            ("s_t", s_t, torch.float32, (_cdiv(rp, 128), cols))):
+        if t is not None:
+            _expect(t, dtype, shape, name)
+
+
+def fp8bw_rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, h=None,
+                           rstd=None, y=None, q=None, s=None, q_t=None,
+                           s_t=None, stream=None, pow2=False):
+    """h = bf16(x + residual) (x itself without a residual), its root-mean-
+    square norm times gamma: as bf16 (y), as row-wise (q, s) and as column-wise
+    codes (q_t, s_t), each if given."""
+    _expect_2d(x, torch.bfloat16, "x")
+    rows, cols = x.shape
+    is_f32 = _gamma_is_f32(gamma, cols)
+    for name, t in (("residual", residual), ("h", h), ("y", y)):
+        if t is not None:
+            _expect(t, torch.bfloat16, (rows, cols), name)
+    if rstd is not None:
+        _expect(rstd, torch.float32, (rows,), "rstd")
+    _expect_codes(q, s, q_t, s_t, rows, cols)
+    _call(_fn("fp8bw_rmsnorm_quantize", pow2),
+          (x, gamma, residual, h, rstd, y, q, s, q_t, s_t), stream, _ptr(x),
+          _ptr(residual), _ptr(gamma), is_f32, rows, cols, eps, _ptr(h),
+          _ptr(rstd), _ptr(y), _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t))
+
+
+def fp8bw_rmsnorm_backward(dy, h, rstd, gamma, dres, dh, dgamma, workspace,
+                           stream=None):
+    """dh (bf16) and dgamma (fp32) of the norm; `workspace` is a uint8 tensor
+    of at least rmsnorm_backward_workspace(rows, cols) bytes."""
+    _expect_2d(h, torch.bfloat16, "h")
+    rows, cols = h.shape
+    is_f32 = _gamma_is_f32(gamma, cols)
+    for name, t in (("dy", dy), ("dres", dres), ("dh", dh)):
+        if t is not None:
+            _expect(t, torch.bfloat16, (rows, cols), name)
+    _expect(rstd, torch.float32, (rows,), "rstd")
+    _expect(dgamma, torch.float32, (cols,), "dgamma")
+    _expect(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    _call("fp8bw_rmsnorm_backward",
+          (dy, h, rstd, gamma, dres, dh, dgamma, workspace), stream, _ptr(dy),
+          _ptr(h), _ptr(rstd), _ptr(gamma), is_f32, _ptr(dres), rows, cols,
+          _ptr(dh), _ptr(dgamma), _ptr(workspace), workspace.numel())
+
+
+def _glu_shape(gu):
+    _expect_2d(gu, torch.bfloat16, "gu")
+    rows, f2 = gu.shape
+    if f2 % 2:
+        raise ValueError("gu: expected an even number of columns, got %d" % f2)
+    return rows, f2 // 2
+
+
+def fp8bw_swiglu_quantize(gu, q, s, q_t=None, s_t=None, stream=None,
+                          pow2=False):
+    """Codes of silu(gate) * up, gu = [gate | up]."""
+    rows, f = _glu_shape(gu)
+    _expect_codes(q, s, q_t, s_t, rows, f)
+    _call(_fn("fp8bw_swiglu_quantize", pow2), (gu, q, s, q_t, s_t), stream,
+          _ptr(gu), rows, f, _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t))
+
+
+def fp8bw_swiglu_backward_quantize(da, gu, q, s, q_t, s_t, stream=None,
+                                   pow2=False):
+    """Codes of [dgate | dup], da being the gradient of silu(gate) * up."""
+    rows, f = _glu_shape(gu)
+    _expect(da, torch.bfloat16, (rows, f), "da")
+    _expect_codes(q, s, q_t, s_t, rows, 2 * f)
+    _call(_fn("fp8bw_swiglu_backward_quantize", pow2),
+          (da, gu, q, s, q_t, s_t), stream, _ptr(da), _ptr(gu), rows, f,
+          _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t))
+
+
+def _workspace_size(name, *args):
+    size = getattr(_lib, name)(*args)
+    if size < 0:
+        raise Fp8bwError(size, name)
+    return size
+
+
+def rmsnorm_backward_workspace(rows, cols):
+    """Bytes of workspace that fp8bw_rmsnorm_backward needs."""
+    return _workspace_size("fp8bw_rmsnorm_backward_workspace", rows, cols)
+
+
+def _ns_jobs(gs, outs):
+    dtype = gs[0].dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("gs: expected bf16 or fp32 tensors, got %s" % dtype)
+    arr = (_native.NsJob * len(gs))()
+    for i, (g, out) in enumerate(zip(gs, outs)):
+        _expect_2d(g, dtype, "gs[%d]" % i)
+        if out is not None:
+            _expect(out, torch.bfloat16, tuple(g.shape), "outs[%d]" % i)
+        arr[i] = _native.NsJob(_ptr(g), g.shape[0], g.shape[1], _ptr(out))
+    return arr, 1 if dtype == torch.float32 else 0
+
+
+def newton_schulz_workspace(gs):
+    """Bytes of workspace that fp8bw_newton_schulz needs for `gs`."""
+    if not gs:
+        return 0
+    arr, _ = _ns_jobs(gs, [None] * len(gs))
+    return _workspace_size("fp8bw_newton_schulz_workspace",
+                           ctypes.cast(arr, ctypes.c_void_p), len(gs))
+
+
+def fp8bw_newton_schulz(gs, outs, workspace, steps=5, coeffs=_NS_COEFFS,
+                        eps=1e-7, stream=None):
+    """Orthogonalise up to 8 matrices of one dtype (bf16 or fp32) into the
+    bf16 `outs`; `workspace` is a uint8 tensor of at least
+    newton_schulz_workspace(gs) bytes."""
+    if len(gs) != len(outs):
+        raise ValueError("gs and outs must have one entry per matrix")
+    if not gs:
+        return
+    arr, is_f32 = _ns_jobs(gs, outs)
+    _expect(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    a, b, c = coeffs
+    _call("fp8bw_newton_schulz", (*gs, *outs, workspace), stream,
+          ctypes.cast(arr, ctypes.c_void_p), len(gs), is_f32, steps, a, b, c,
+          eps, _ptr(workspace), workspace.numel())
 
 
 # ----------------------------------------------------------- allocating helpers
+
+def _allocating(stream, dev):
+    """Context whose allocations on `dev` belong to the stream a call runs on,
+    so that memory freed on another stream is not reused under it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle \
+            else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+class Codes(NamedTuple):
+    """E4M3 codes and scales of a [rows, cols] tensor whose rows are padded to
+    rp = 16 * ceil(rows / 16): row-wise q [rp, cols], s [ceil(cols/128)][rp];
+    column-wise q_t [cols, rp], s_t [ceil(rp/128)][cols] (None if not asked
+    for)."""
+    q: torch.Tensor
+    s: torch.Tensor
+    q_t: Optional[torch.Tensor]
+    s_t: Optional[torch.Tensor]
+
+
+class NormCodes(NamedTuple):
+    """Codes of a norm's output (see Codes), with what its backward pass
+    needs: h (the sum that was normalised) and rstd."""
+    q: torch.Tensor
+    s: torch.Tensor
+    q_t: Optional[torch.Tensor]
+    s_t: Optional[torch.Tensor]
+    h: torch.Tensor
+    rstd: torch.Tensor
+
+
+def _empty_codes(rows, cols, dev, colwise):
+    rp = _pad16(rows)
+    q = torch.empty((rp, cols), dtype=torch.uint8, device=dev)
+    s = torch.empty((_cdiv(cols, 128), rp), dtype=torch.float32, device=dev)
+    if not colwise:
+        return q, s, None, None
+    return (q, s, torch.empty((cols, rp), dtype=torch.uint8, device=dev),
+            torch.empty((_cdiv(rp, 128), cols), dtype=torch.float32,
+                        device=dev))
+
+
+def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, colwise=False,
+                     stream=None, pow2=False):
+    """-> NormCodes of the root-mean-square norm of x (+ residual) times
+    gamma; h is the bf16 sum (x itself without a residual)."""
+    _expect_2d(x, torch.bfloat16, "x")
+    rows, cols = x.shape
+    dev = x.device
+    with _allocating(stream, dev):
+        h = x if residual is None else torch.empty_like(x)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        codes = _empty_codes(rows, cols, dev, colwise)
+    fp8bw_rmsnorm_quantize(x, gamma, residual, eps,
+                           None if residual is None else h, rstd, None,
+                           *codes, stream=stream, pow2=pow2)
+    return NormCodes(*codes, h, rstd)
+
+
+def rmsnorm(x, gamma, residual=None, eps=1e-6, stream=None):
+    """-> (y, h, rstd): the norm's bf16 output without quantisation (for what
+    is not an FP8 linear: a final norm, a router)."""
+    _expect_2d(x, torch.bfloat16, "x")
+    with _allocating(stream, x.device):
+        h = x if residual is None else torch.empty_like(x)
+        y = torch.empty_like(x)
+        rstd = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    fp8bw_rmsnorm_quantize(x, gamma, residual, eps,
+                           None if residual is None else h, rstd, y,
+                           stream=stream)
+    return y, h, rstd
+
+
+def rmsnorm_backward(dy, h, rstd, gamma, dres=None, stream=None):
+    """-> (dh, dgamma): the gradient of x (and of the residual), bf16, and the
+    fp32 gradient of gamma. `dres` is the gradient that reaches h directly."""
+    _expect_2d(h, torch.bfloat16, "h")
+    rows, cols = h.shape
+    dev = h.device
+    with _allocating(stream, dev):
+        dh = torch.empty_like(h)
+        dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
+        ws = torch.empty((rmsnorm_backward_workspace(rows, cols),),
+                         dtype=torch.uint8, device=dev)
+    fp8bw_rmsnorm_backward(dy, h, rstd, gamma, dres, dh, dgamma, ws, stream)
+    return dh, dgamma
+
+
+def swiglu_quantize(gu, colwise=False, stream=None, pow2=False):
+    """-> Codes of silu(gate) * up, gu = [gate | up] ([rows, 2f])."""
+    rows, f = _glu_shape(gu)
+    with _allocating(stream, gu.device):
+        codes = _empty_codes(rows, f, gu.device, colwise)
+    fp8bw_swiglu_quantize(gu, *codes, stream=stream, pow2=pow2)
+    return Codes(*codes)
+
+
+def swiglu_backward_quantize(da, gu, stream=None, pow2=False):
+    """-> Codes (both ways) of [dgate | dup] ([rows, 2f])."""
+    rows, f = _glu_shape(gu)
+    with _allocating(stream, gu.device):
+        codes = _empty_codes(rows, 2 * f, gu.device, True)
+    fp8bw_swiglu_backward_quantize(da, gu, *codes, stream=stream, pow2=pow2)
+    return Codes(*codes)
+
+
+def newton_schulz_batch(gs, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
+    """-> [bf16 orthogonalised update] for each matrix of `gs` (all bf16 or
+    all fp32), up to 8 per launch; the workspace is shared by the launches."""
+    gs = list(gs)
+    if not gs:
+        return []
+    parts = [gs[i:i + _NS_MAX_JOBS] for i in range(0, len(gs), _NS_MAX_JOBS)]
+    dev = _device_of(gs)
+    with _allocating(stream, dev):
+        outs = [torch.empty(tuple(g.shape), dtype=torch.bfloat16, device=dev)
+                for g in gs]
+        ws = torch.empty((max(newton_schulz_workspace(p) for p in parts),),
+                         dtype=torch.uint8, device=dev)
+    for i, part in enumerate(parts):
+        fp8bw_newton_schulz(part, outs[i * _NS_MAX_JOBS:(i + 1) * _NS_MAX_JOBS],
+                            ws, steps, coeffs, eps, stream)
+    return outs
+
+
+def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
+    """-> the bf16 orthogonalised update of one matrix."""
+    return newton_schulz_batch([g], steps, coeffs, eps, stream)[0]
+
 
 def quantize_rowwise(x, stream=None, pow2=False):
     rows, cols = x.shape
