@@ -477,29 +477,30 @@ int64_t ns_tiles(const NsGemm& g, int bn, bool sym) {
   return tm * tn - per * (tm * (tm - 1) / 2);
 }
 
-// The longest cluster's work under the kernel's tile order, in 256-column
-// chunk units (a tile also costs about two chunks of pipeline fill).
+// The longest cluster's time under the kernel's tile order, in chunks of a
+// 256-wide tile. Operands reach the SMs at 8.7 TB/s at most (measured, whatever
+// the tile width, ring depth or tile order), which is what a chunk costs:
+// 32 KB per CTA with 256 columns, 24 KB with 128. A tile also costs about two
+// chunks of pipeline fill.
 double ns_makespan(const NsGemm* g, int count, int bn, bool sym, int clusters) {
+  const double chunk = bn == 256 ? 1.0 : 0.75;
   int64_t total = 0;
-  for (int i = 0; i < count; ++i) total += ns_tiles(g[i], bn, sym);
-  const int64_t waves = cdiv(total, clusters);
-  if (waves > 16) {      // long: the sum decides
-    double sum = 0.0;
-    for (int i = 0; i < count; ++i)
-      sum += static_cast<double>(ns_tiles(g[i], bn, sym)) * (cdiv(g[i].kc, ns::BK) + 2) * bn;
-    return sum / 256.0 / clusters;
+  double sum = 0.0;
+  for (int i = 0; i < count; ++i) {
+    total += ns_tiles(g[i], bn, sym);
+    sum += static_cast<double>(ns_tiles(g[i], bn, sym)) * (cdiv(g[i].kc, ns::BK) + 2) * chunk;
   }
-  auto cost_of = [&](int64_t t) {
-    int i = 0;
-    while (t >= ns_tiles(g[i], bn, sym)) t -= ns_tiles(g[i++], bn, sym);
-    return static_cast<double>(cdiv(g[i].kc, ns::BK) + 2) * bn / 256.0;
-  };
+  const int64_t waves = cdiv(total, clusters);
+  if (waves > 16) return sum / clusters;      // the last wave hardly counts
   double worst = 0.0;
   for (int c = 0; c < clusters; ++c) {
     double w = 0.0;
     for (int64_t k = 0; k < waves; ++k) {
-      const int64_t t = k * clusters + ((k & 1) ? clusters - 1 - c : c);
-      if (t < total) w += cost_of(t);
+      int64_t t = k * clusters + ((k & 1) ? clusters - 1 - c : c);
+      if (t >= total) continue;
+      int i = 0;
+      while (t >= ns_tiles(g[i], bn, sym)) t -= ns_tiles(g[i++], bn, sym);
+      w += static_cast<double>(cdiv(g[i].kc, ns::BK) + 2) * chunk;
     }
     worst = std::max(worst, w);
   }
@@ -564,7 +565,7 @@ int ns_prepare(NsLaunch* l, const NsGemm* in, int count, const Device& dev) {
   if (st == FP8BW_OK) st = ns_clusters<128, MODE>(dev, &c128);
   if (st != FP8BW_OK) return st;
   // 128-wide tiles where they spread the work better over the clusters
-  l->bn = ns_makespan(g, count, 128, kSym, c128) < 0.95 * ns_makespan(g, count, 256, kSym, c256)
+  l->bn = ns_makespan(g, count, 128, kSym, c128) < 0.97 * ns_makespan(g, count, 256, kSym, c256)
               ? 128
               : 256;
   l->clusters = l->bn == 256 ? c256 : c128;

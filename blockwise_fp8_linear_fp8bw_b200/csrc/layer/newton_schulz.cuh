@@ -75,6 +75,7 @@ struct Layout {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kSlots = 3;                 // C / result boxes per warp
+  static constexpr int kAhead = kSlots - 1;        // C boxes requested ahead
   static constexpr int kBoxBytes = 32 * 32 * 2;
   static constexpr int kSlotBytes = 2 * kBoxBytes;
   static constexpr int kSlotOff = kRingBytes;
@@ -101,6 +102,17 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, ui
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -269,7 +281,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue (even CTA)
-    if (leader && lane == 0) {
+    // The whole warp walks the loop, so that addresses and descriptors stay
+    // warp-uniform, and one elected lane issues. The next chunk's barrier is
+    // probed before this chunk's MMAs are issued: the probe's round trip (about
+    // 150 cycles) then runs under the issue instead of adding to it.
+    if (leader) {
+      const bool elected = elect_one();
       uint32_t it = 0, tc = 0;
       bool ok = true;
       for (int k = 0; ok && k < waves; ++k) {
@@ -279,6 +296,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int chunks = args.job[j].chunks;
         const bool a_mn = args.job[j].a_mn != 0, b_mn = args.job[j].b_mn != 0;
         const uint32_t idesc = idesc_f16(2 * BM, BN, a_mn, b_mn);
+        // K = 16 per instruction: 32 bytes along a K-major row, or 16 rows
+        // of 128 bytes of an MN-major tile (64-element atoms 8 KB apart)
+        const uint64_t ad0 = a_mn ? desc_mnmajor_sw128(sbase, 64 * BK * 2) : desc_kmajor_sw128(sbase);
+        const uint64_t bd0 = b_mn ? desc_mnmajor_sw128(sbase + L::kABytes, 64 * BK * 2)
+                                  : desc_kmajor_sw128(sbase + L::kABytes);
+        const uint64_t as = a_mn ? (16 * 128) >> 4 : 32 >> 4;
+        const uint64_t bs = b_mn ? (16 * 128) >> 4 : 32 >> 4;
         const int tb = tc % kBufs;
         const uint32_t tu = tc / kBufs;
         ++tc;
@@ -286,36 +310,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(tb * BN);
+        bool ready = false;
         for (int c = 0; c < chunks; ++c, ++it) {
           const int s = it % kStages;
-          if (!mbar_wait(full_bar(s), (it / kStages) & 1u, abort_flag, kErrTimeoutMma)) {
+          if (!ready && !mbar_wait(full_bar(s), (it / kStages) & 1u, abort_flag, kErrTimeoutMma)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = sbase + s * L::kStageBytes;
-          const uint32_t b_addr = a_addr + L::kABytes;
-          // K = 16 per instruction: 32 bytes along a K-major row, or 16 rows
-          // of 128 bytes of an MN-major tile (64-element atoms 8 KB apart)
-          const uint64_t ad = a_mn ? desc_mnmajor_sw128(a_addr, 64 * BK * 2) : desc_kmajor_sw128(a_addr);
-          const uint64_t bd = b_mn ? desc_mnmajor_sw128(b_addr, 64 * BK * 2) : desc_kmajor_sw128(b_addr);
-          const uint64_t as = a_mn ? (16 * 128) >> 4 : 32 >> 4;
-          const uint64_t bs = b_mn ? (16 * 128) >> 4 : 32 >> 4;
+          const uint32_t nx = it + 1;
+          ready = c + 1 < chunks && mbar_try_wait(full_bar(nx % kStages), (nx / kStages) & 1u);
+          const uint64_t off = static_cast<uint64_t>(s * L::kStageBytes) >> 4;
+          const uint64_t ad = ad0 + off, bd = bd0 + off;
+          if (elected) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, idesc, c > 0 || kk > 0 ? 1u : 0u);
-          mma_commit_pair(empty_bar(s), 0x3);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, idesc, c > 0 || kk > 0 ? 1u : 0u);
+            mma_commit_pair(empty_bar(s), 0x3);
+          }
+          __syncwarp();
         }
-        if (ok) mma_commit_pair(tfull_bar(tb), 0x3);
+        if (ok && elected) mma_commit_pair(tfull_bar(tb), 0x3);
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && elected) {
         mma_commit_pair(drain_bar, 0x1);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
       }
+      __syncwarp();
     }
   } else if (warp >= kFirstEpiWarp) {
     // ------------------------------------------------------------ epilogue
@@ -346,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto load_c = [&](int gi) {
         const int s = loads % L::kSlots;
         if (lane == 0) {
-          bulk_wait_group_read<1>();
+          bulk_wait_group_read<L::kSlots - L::kAhead>();
           const uint32_t dst = slot0 + s * L::kSlotBytes;
           mbar_arrive_expect_tx(slot_bar(ew, s), kHasLo ? 2 * L::kBoxBytes : L::kBoxBytes);
           tma_load_2d(dst, &maps.c[j], slot_bar(ew, s), x0 + gi * 32, y0);
@@ -358,8 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr (kHasC) {
         if (boxes > 0) {
           if (lane == 0) bulk_wait_group_read<0>();
-          load_c(0);
-          if (boxes > 1) load_c(1);
+          for (int gi = 0; gi < L::kAhead && gi < boxes; ++gi) load_c(gi);
         }
       }
       const int tb = tc % kBufs;
@@ -482,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bulk_commit_group();
         }
         if constexpr (kHasC) {
-          if (gi + 2 < boxes) load_c(gi + 2);
+          if (gi + L::kAhead < boxes) load_c(gi + L::kAhead);
         }
       }
       if (!ok) break;

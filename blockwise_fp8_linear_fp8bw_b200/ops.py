@@ -381,6 +381,40 @@ def _pad16(rows):
     return (rows + 15) // 16 * 16
 
 
+def _input(t, dtype, shape, name, dev):
+    """Device pointer of a contiguous input of that dtype and shape on `dev`."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s: expected %s %s, got %s %s" %
+                         (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if t.device != dev:
+        raise ValueError("expected tensors on one CUDA device, got %s and %s"
+                         % (dev, t.device))
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _need_cuda(dev):
+    if dev.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
+
+
+def _run(name, dev, stream, *args):
+    """_call for the allocating helpers below, whose tensors are known to be on
+    `dev` (their calls can be a few microseconds long, most of which would be
+    the checks of buffers that were just allocated)."""
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None \
+        else _stream(stream, dev)
+    fn = getattr(_lib, name)
+    if dev.index == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != FP8BW_OK:
+        _check(status, name)
+
+
 def _gamma_is_f32(gamma, cols):
     if gamma.dtype not in (torch.bfloat16, torch.float32) or \
             tuple(gamma.shape) != (cols,):
@@ -528,11 +562,14 @@ def fp8bw_newton_schulz(gs, outs, workspace, steps=5, coeffs=_NS_COEFFS,
 
 # ----------------------------------------------------------- allocating helpers
 
+_HERE = contextlib.nullcontext()
+
+
 def _allocating(stream, dev):
     """Context whose allocations on `dev` belong to the stream a call runs on,
     so that memory freed on another stream is not reused under it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not hasattr(stream, "cuda_stream"):
         handle = int(stream)
         stream = torch.cuda.ExternalStream(handle, device=dev) if handle \
@@ -563,77 +600,99 @@ class NormCodes(NamedTuple):
 
 
 def _empty_codes(rows, cols, dev, colwise):
+    """Codes' buffers and their device pointers."""
     rp = _pad16(rows)
     q = torch.empty((rp, cols), dtype=torch.uint8, device=dev)
     s = torch.empty((_cdiv(cols, 128), rp), dtype=torch.float32, device=dev)
     if not colwise:
-        return q, s, None, None
-    return (q, s, torch.empty((cols, rp), dtype=torch.uint8, device=dev),
-            torch.empty((_cdiv(rp, 128), cols), dtype=torch.float32,
-                        device=dev))
+        return (q, s, None, None), (q.data_ptr(), s.data_ptr(), None, None)
+    q_t = torch.empty((cols, rp), dtype=torch.uint8, device=dev)
+    s_t = torch.empty((_cdiv(rp, 128), cols), dtype=torch.float32, device=dev)
+    return (q, s, q_t, s_t), (q.data_ptr(), s.data_ptr(), q_t.data_ptr(),
+                              s_t.data_ptr())
+
+
+def _norm_inputs(x, gamma, residual):
+    _expect_2d(x, torch.bfloat16, "x")
+    dev, shape = x.device, x.shape
+    is_f32 = _gamma_is_f32(gamma, shape[1])
+    return (dev, shape, is_f32, _input(x, torch.bfloat16, shape, "x", dev),
+            _input(gamma, gamma.dtype, gamma.shape, "gamma", dev),
+            None if residual is None else
+            _input(residual, torch.bfloat16, shape, "residual", dev))
 
 
 def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, colwise=False,
                      stream=None, pow2=False):
     """-> NormCodes of the root-mean-square norm of x (+ residual) times
     gamma; h is the bf16 sum (x itself without a residual)."""
-    _expect_2d(x, torch.bfloat16, "x")
-    rows, cols = x.shape
-    dev = x.device
+    dev, (rows, cols), is_f32, px, pg, pr = _norm_inputs(x, gamma, residual)
+    _need_cuda(dev)
     with _allocating(stream, dev):
-        h = x if residual is None else torch.empty_like(x)
+        h = x if pr is None else torch.empty_like(x)
         rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-        codes = _empty_codes(rows, cols, dev, colwise)
-    fp8bw_rmsnorm_quantize(x, gamma, residual, eps,
-                           None if residual is None else h, rstd, None,
-                           *codes, stream=stream, pow2=pow2)
+        codes, ptrs = _empty_codes(rows, cols, dev, colwise)
+    _run(_fn("fp8bw_rmsnorm_quantize", pow2), dev, stream, px, pr, pg, is_f32,
+         rows, cols, eps, None if pr is None else h.data_ptr(),
+         rstd.data_ptr(), None, *ptrs)
     return NormCodes(*codes, h, rstd)
 
 
 def rmsnorm(x, gamma, residual=None, eps=1e-6, stream=None):
     """-> (y, h, rstd): the norm's bf16 output without quantisation (for what
     is not an FP8 linear: a final norm, a router)."""
-    _expect_2d(x, torch.bfloat16, "x")
-    with _allocating(stream, x.device):
-        h = x if residual is None else torch.empty_like(x)
+    dev, (rows, cols), is_f32, px, pg, pr = _norm_inputs(x, gamma, residual)
+    _need_cuda(dev)
+    with _allocating(stream, dev):
+        h = x if pr is None else torch.empty_like(x)
         y = torch.empty_like(x)
-        rstd = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
-    fp8bw_rmsnorm_quantize(x, gamma, residual, eps,
-                           None if residual is None else h, rstd, y,
-                           stream=stream)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    _run("fp8bw_rmsnorm_quantize", dev, stream, px, pr, pg, is_f32, rows, cols,
+         eps, None if pr is None else h.data_ptr(), rstd.data_ptr(),
+         y.data_ptr(), None, None, None, None)
     return y, h, rstd
 
 
 def rmsnorm_backward(dy, h, rstd, gamma, dres=None, stream=None):
     """-> (dh, dgamma): the gradient of x (and of the residual), bf16, and the
     fp32 gradient of gamma. `dres` is the gradient that reaches h directly."""
-    _expect_2d(h, torch.bfloat16, "h")
-    rows, cols = h.shape
-    dev = h.device
+    dev, (rows, cols), is_f32, ph, pg, pr = _norm_inputs(h, gamma, dres)
+    pdy = _input(dy, torch.bfloat16, h.shape, "dy", dev)
+    ps = _input(rstd, torch.float32, (rows,), "rstd", dev)
+    _need_cuda(dev)
+    size = rmsnorm_backward_workspace(rows, cols)
     with _allocating(stream, dev):
         dh = torch.empty_like(h)
         dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
-        ws = torch.empty((rmsnorm_backward_workspace(rows, cols),),
-                         dtype=torch.uint8, device=dev)
-    fp8bw_rmsnorm_backward(dy, h, rstd, gamma, dres, dh, dgamma, ws, stream)
+        ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+    _run("fp8bw_rmsnorm_backward", dev, stream, pdy, ph, ps, pg, is_f32, pr,
+         rows, cols, dh.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), size)
     return dh, dgamma
 
 
 def swiglu_quantize(gu, colwise=False, stream=None, pow2=False):
     """-> Codes of silu(gate) * up, gu = [gate | up] ([rows, 2f])."""
     rows, f = _glu_shape(gu)
-    with _allocating(stream, gu.device):
-        codes = _empty_codes(rows, f, gu.device, colwise)
-    fp8bw_swiglu_quantize(gu, *codes, stream=stream, pow2=pow2)
+    dev = gu.device
+    pg = _input(gu, torch.bfloat16, gu.shape, "gu", dev)
+    _need_cuda(dev)
+    with _allocating(stream, dev):
+        codes, ptrs = _empty_codes(rows, f, dev, colwise)
+    _run(_fn("fp8bw_swiglu_quantize", pow2), dev, stream, pg, rows, f, *ptrs)
     return Codes(*codes)
 
 
 def swiglu_backward_quantize(da, gu, stream=None, pow2=False):
     """-> Codes (both ways) of [dgate | dup] ([rows, 2f])."""
     rows, f = _glu_shape(gu)
-    with _allocating(stream, gu.device):
-        codes = _empty_codes(rows, 2 * f, gu.device, True)
-    fp8bw_swiglu_backward_quantize(da, gu, *codes, stream=stream, pow2=pow2)
+    dev = gu.device
+    pg = _input(gu, torch.bfloat16, gu.shape, "gu", dev)
+    pd = _input(da, torch.bfloat16, (rows, f), "da", dev)
+    _need_cuda(dev)
+    with _allocating(stream, dev):
+        codes, ptrs = _empty_codes(rows, 2 * f, dev, True)
+    _run(_fn("fp8bw_swiglu_backward_quantize", pow2), dev, stream, pd, pg,
+         rows, f, *ptrs)
     return Codes(*codes)
 
 
