@@ -165,21 +165,25 @@ int launch_norm_rows(NormArgs a, cudaStream_t stream) {
   a.tpr = threads_per_row(a.cols / 8, V);
   const int groups = std::max(1, 256 / a.tpr);
   const int64_t blocks = cdiv(a.row_end - a.row0, groups);
-  return launched(launch_kernel(rmsnorm_row_kernel<V, POW2>, dim3(static_cast<unsigned>(blocks)),
-                                dim3(groups * a.tpr), 0, stream, a));
+  const auto kernel = a.cols == 8 * static_cast<int64_t>(V) * a.tpr
+                          ? rmsnorm_row_kernel<V, true, POW2>
+                          : rmsnorm_row_kernel<V, false, POW2>;
+  return launched(launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(groups * a.tpr),
+                                0, stream, a));
 }
 
 template <bool POW2>
 int norm_rows(const NormArgs& a, const Device& dev, cudaStream_t stream) {
   const int64_t chunks = a.cols / 8;
-  // Many rows: one warp per row where its registers suffice (no block barrier,
-  // all of a row's loads in flight at once). Few rows: the most threads per
-  // row, for latency.
+  // Many rows: four chunks per thread (64 registers: 32 warps per SM with up to
+  // eight 16-byte loads each in flight); two and one where a row has too few.
+  // Measured at 16384 x 2048 with 1, 2, 4, 8 chunks: 54, 50, 48, 61 us. Few
+  // rows: the most threads per row, for latency (512 x 2048: 3.9 us with one
+  // chunk, 5.0 with four).
   const bool many = a.row_end - a.row0 > 4 * static_cast<int64_t>(dev.sm_count);
-  const int64_t per = many ? 32 : 1024;
-  if (chunks <= per) return launch_norm_rows<1, POW2>(a, stream);
-  if (many && chunks <= 2 * per) return launch_norm_rows<2, POW2>(a, stream);
-  if (chunks <= (many ? 4 * per : 2 * per)) return launch_norm_rows<4, POW2>(a, stream);
+  if (chunks <= (many ? 32 : 1024)) return launch_norm_rows<1, POW2>(a, stream);
+  if (many && chunks <= 64) return launch_norm_rows<2, POW2>(a, stream);
+  if (chunks <= 2048) return launch_norm_rows<4, POW2>(a, stream);
   return launch_norm_rows<8, POW2>(a, stream);
 }
 
@@ -251,15 +255,13 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
     c.gamma = gamma;
     c.gamma_f32 = a.gamma_f32;
     c.rows = rows;
-    c.rows_pad = rp;
     c.cols = cols;
     c.tr0 = static_cast<int>(r0 / 128);
     c.tiles_r = static_cast<int>(cdiv(a.row_end - r0, 128));
     c.tiles_c = static_cast<int>(cdiv(cols, 128));
-    c.q_t = q_t;
-    c.s_t = s_t;
+    c.out = CodesOut{nullptr, nullptr, q_t, s_t, rp, cols};
     const int tiles = c.tiles_r * c.tiles_c;
-    st = launched(launch_kernel(norm_col_kernel<POW2>, dim3(std::min(tiles, 2 * dev.sm_count)),
+    st = launched(launch_kernel(norm_col_kernel<POW2>, dim3(std::min(tiles, dev.sm_count)),
                                 dim3(kTileThreads), NormColSmem::kAlloc, cs, map, c));
     if (st != FP8BW_OK) return st;
   }
@@ -368,10 +370,10 @@ int swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, flo
   static DevicePrep prep;
   st = allow_smem(prep, dev.ordinal, swiglu_tile_kernel<POW2>, GluFwdSmem::kAlloc);
   if (st != FP8BW_OK) return st;
-  const GluTileArgs a{rp, f, static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
-                      q, s, q_t, s_t};
+  const GluTileArgs a{static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
+                      CodesOut{q, s, q_t, s_t, rp, f}};
   const int tiles = a.tiles_r * a.tiles_c;
-  return launched(launch_kernel(swiglu_tile_kernel<POW2>, dim3(std::min(tiles, 2 * dev.sm_count)),
+  return launched(launch_kernel(swiglu_tile_kernel<POW2>, dim3(std::min(tiles, dev.sm_count)),
                                 dim3(kTileThreads), GluFwdSmem::kAlloc, cs, mg, mu, a));
 }
 
@@ -393,15 +395,15 @@ int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t row
   st = current_device(&dev);
   if (st != FP8BW_OK || n == 0) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  GluTileArgs a{rp, f, static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
-                q, s, q_t, s_t};
+  GluTileArgs a{static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
+                CodesOut{q, s, q_t, s_t, rp, 2 * f}};
   if (f % 128 != 0) {
     a.tiles_c = static_cast<int>(cdiv(2 * f, 128));
-    const GluRaggedArgs r{gu, da, rows, a};
+    const GluRaggedArgs r{gu, da, rows, f, a};
     const int tiles = a.tiles_r * a.tiles_c;
     return launched(launch_kernel(swiglu_bwd_ragged_kernel<POW2>,
-                                  dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kTileThreads),
-                                  TileEmit::kBytes + 128, cs, r));
+                                  dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kWorkThreads),
+                                  TileEmit<1, true, false>::kBytes + 128, cs, r));
   }
   CUtensorMap mg, mu, md;
   st = encode_tiles(&mg, gu, rows, f, 4 * f);
@@ -413,7 +415,7 @@ int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t row
   if (st != FP8BW_OK) return st;
   const int tiles = a.tiles_r * a.tiles_c;
   return launched(launch_kernel(swiglu_bwd_tile_kernel<POW2>,
-                                dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kTileThreads),
+                                dim3(std::min(tiles, dev.sm_count)), dim3(kTileThreads),
                                 GluBwdSmem::kAlloc, cs, mg, mu, md, a));
 }
 

@@ -3,7 +3,7 @@
 //
 //   h    = bf16(x + residual)                (h = x without a residual)
 //   rstd = 1 / sqrt(mean_c h^2 + eps)        fp32
-//   y    = (h * rstd) * gamma                fp32
+//   y    = h * rstd * gamma                  fp32
 //   codes and scales of y as the quantisers write them, but of the fp32 y:
 //   the only rounding of y is the one to E4M3.
 // Backward, with dy the gradient of y and dres the one that reaches h directly
@@ -26,11 +26,6 @@ namespace fp8bw {
 namespace layer {
 
 // ---------------------------------------------------------------- helpers
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
 __device__ __forceinline__ uint4 ld16(const void* p) {
   return *reinterpret_cast<const uint4*>(p);
 }
@@ -74,6 +69,18 @@ __device__ __forceinline__ void load_gamma8(const void* gamma, int is_f32, int64
   }
 }
 
+// The same for four columns.
+__device__ __forceinline__ void load_gamma4(const void* gamma, int is_f32, int64_t c,
+                                            float (&g)[4]) {
+  if (is_f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(gamma) + c));
+    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+  } else {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(gamma) + c));
+    g[0] = bf16_lo(w.x), g[1] = bf16_hi(w.x), g[2] = bf16_lo(w.y), g[3] = bf16_hi(w.y);
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -99,8 +106,22 @@ struct NormArgs {
 
 constexpr int kNormMaxWarps = 32;
 
+// Element-wise bf16 sums of two packed vectors, each rounded once.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hadd2_rn(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                      *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z),
+                    add_bf16x2(a.w, b.w));
+}
+
 // V chunks of 8 columns per thread; blockDim = groups x tpr, one row each.
-template <int V, bool POW2>
+// FULL: the row is exactly V x tpr chunks. h * gamma and the groups' maxima of
+// it are formed before rstd is known, so all that is left after the row sum is
+// one product per element: codes are E4M3(h gamma * (rstd * qscale)).
+template <int V, bool FULL, bool POW2>
 __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
     rmsnorm_row_kernel(const NormArgs a) {
   __shared__ float part[kNormMaxWarps];
@@ -110,90 +131,105 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
   const int grp = threadIdx.x / tpr;
   const int t = threadIdx.x - grp * tpr;
   const int groups = blockDim.x / tpr;
+  const int lane = threadIdx.x & 31;
   const int64_t row = a.row0 + static_cast<int64_t>(blockIdx.x) * groups + grp;
   const bool live = row < a.rows && row < a.row_end;
   const int chunks = static_cast<int>(a.cols >> 3);
   const int64_t base = row * a.cols;
+  auto has = [&](int v) { return FULL || t + v * tpr < chunks; };
+  auto col = [&](int v) { return 8 * static_cast<int64_t>(t + v * tpr); };
 
   uint4 h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = t + v * tpr;
-    h[v] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && c < chunks) h[v] = ld16_stream(a.x + base + 8 * static_cast<int64_t>(c));
-  }
+  for (int v = 0; v < V; ++v)
+    h[v] = live && has(v) ? ld16_stream(a.x + base + col(v)) : make_uint4(0u, 0u, 0u, 0u);
   if (a.residual != nullptr) {
     uint4 r[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = t + v * tpr;
-      r[v] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && c < chunks) r[v] = ld16_stream(a.residual + base + 8 * static_cast<int64_t>(c));
-    }
+    for (int v = 0; v < V; ++v)
+      r[v] = live && has(v) ? ld16_stream(a.residual + base + col(v)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * tpr;
-      float f[8], e[8];
-      unpack8(h[v], f);
-      unpack8(r[v], e);
-      h[v] = make_uint4(pack_bf16(f[0] + e[0], f[1] + e[1]), pack_bf16(f[2] + e[2], f[3] + e[3]),
-                        pack_bf16(f[4] + e[4], f[5] + e[5]), pack_bf16(f[6] + e[6], f[7] + e[7]));
-      if (live && c < chunks)
-        *reinterpret_cast<uint4*>(a.h + base + 8 * static_cast<int64_t>(c)) = h[v];
+      h[v] = add_bf16x8(h[v], r[v]);
+      if (live && has(v)) *reinterpret_cast<uint4*>(a.h + base + col(v)) = h[v];
     }
   }
 
-  float ss = 0.0f;
+  float ss = 0.0f, y[V][8], m[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float f[8];
-    unpack8(h[v], f);
+    float g[8];
+    if (has(v)) load_gamma8(a.gamma, a.gamma_f32, col(v), g);
+    else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+      for (int j = 0; j < 8; ++j) g[j] = 0.0f;
+    }
+    unpack8(h[v], y[v]);
+    m[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      ss = fmaf(y[v][j], y[v][j], ss);
+      ss = fmaf(y[v][j + 1], y[v][j + 1], ss);
+      fmul2(y[v][j], y[v][j + 1], y[v][j], y[v][j + 1], g[j], g[j + 1]);
+      m[v] = max3_abs(m[v], y[v][j], y[v][j + 1]);
+    }
   }
+  // group maxima over the 16 lanes of a half-warp: lanes halve the groups they
+  // hold as they exchange, so that each ends up with one of the V
+#pragma unroll
+  for (int half = V / 2, bit = 8; bit >= 1; bit >>= 1) {
+    if (half >= 1) {
+      const bool up = (lane & bit) != 0;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const float send = up ? m[i] : m[i + half];
+        const float keep = up ? m[i + half] : m[i];
+        m[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, bit));
+      }
+      half >>= 1;
+    } else {
+      m[0] = fmaxf(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], bit));
+    }
+  }
+  constexpr int kShare = 16 / V;               // lanes that hold the same group
+  const int mine = (lane & 15) / kShare;       // which one
+
   ss = warp_sum(ss);
   const int wpr = tpr >> 5;
   if (wpr > 1) {
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) part[warp] = ss;
+    if (lane == 0) part[threadIdx.x >> 5] = ss;
     __syncthreads();
     ss = 0.0f;
     for (int w = 0; w < wpr; ++w) ss += part[grp * wpr + w];
   }
   const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
   if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
-  if (a.q == nullptr && a.y == nullptr) return;
 
+  if (a.y != nullptr && live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!has(v)) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(y[v][2 * j] * rstd, y[v][2 * j + 1] * rstd);
+      *reinterpret_cast<uint4*>(a.y + base + col(v)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (a.q == nullptr) return;
+  float qs, s;
+  scale_of<POW2>(m[0] * rstd, qs, s);
+  const float f = qs * rstd;
+  const bool out = row < a.row_end;
+  const int64_t first = (t & ~15) + mine * tpr;       // first chunk of this lane's group
+  if ((lane & (kShare - 1)) == 0 && out && (FULL || first < chunks))
+    a.s[(first >> 4) * a.rows_pad + row] = s;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = t + v * tpr;
-    const bool in = c < chunks;
-    float y[8], g[8];
-    unpack8(h[v], y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-    if (live && in) load_gamma8(a.gamma, a.gamma_f32, 8 * static_cast<int64_t>(c), g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = live && in ? (y[j] * rstd) * g[j] : 0.0f;
-    if (a.y != nullptr && live && in)
-      *reinterpret_cast<uint4*>(a.y + base + 8 * static_cast<int64_t>(c)) =
-          make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                     pack_bf16(y[6], y[7]));
-    if (a.q != nullptr) {
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(y[j]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      float qs, s;
-      scale_of<POW2>(m, qs, s);
-      if (in && row < a.row_end) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= qs;
-        *reinterpret_cast<uint2*>(a.q + base + 8 * static_cast<int64_t>(c)) = encode8(y);
-        if ((c & 15) == 0) a.s[static_cast<int64_t>(c >> 4) * a.rows_pad + row] = s;
-      }
-    }
+    const float k = __shfl_sync(0xFFFFFFFFu, f, (lane & 16) | (v * kShare));
+    uint2 w;
+    w.x = encode4(y[v][0], y[v][1], y[v][2], y[v][3], k);
+    w.y = encode4(y[v][4], y[v][5], y[v][6], y[v][7], k);
+    if (out && has(v)) *reinterpret_cast<uint2*>(a.q + base + col(v)) = w;
   }
 }
 
@@ -203,94 +239,69 @@ struct NormColArgs {
   const float* rstd;
   const void* gamma;
   int gamma_f32;
-  int64_t rows, rows_pad, cols;
+  int64_t rows, cols;
   int tr0;                    // first row tile of this launch
   int tiles_r, tiles_c;
-  uint8_t* q_t;
-  float* s_t;
+  CodesOut out;
 };
 
+using NormRing = TileRing<1, 5>;
 struct NormColSmem {
-  static constexpr int kIn = 0;                                  // 2 x 32 KB
-  static constexpr int kEmit = 2 * kTileBytes;
-  static constexpr int kBar = kEmit + TileEmit::kBytes;
-  static constexpr int kBytes = kBar + 32;
-  static constexpr int kAlloc = kBytes + 128;
+  static constexpr int kEmit = (NormRing::kBytes + 127) / 128 * 128;
+  static constexpr int kAlloc = kEmit + TileEmit<1, false, false>::kBytes + 128;
 };
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
     norm_col_kernel(const __grid_constant__ CUtensorMap map_h, const NormColArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar0 = sbase + NormColSmem::kBar;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + NormColSmem::kBar + 16);
-  const int t = threadIdx.x, rb = t >> 4, cg = t & 15;
+  const NormRing ring(smem);
   const int num_tiles = a.tiles_r * a.tiles_c;
-  if (t == 0) {
-    mbar_init(bar0, 1);
-    mbar_init(bar0 + 8, 1);
-    *abort_flag = 0u;
-    fence_mbar_init();
+  if (threadIdx.x == 0) {
+    ring.init();
     prefetch_tmap(&map_h);
   }
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  // last rows first: they are the most recently written
-  auto load = [&](int k, int b) {
-    const int tile = num_tiles - 1 - k;
-    mbar_arrive_expect_tx(bar0 + 8u * b, kTileBytes);
-    tma_load_2d(sbase + NormColSmem::kIn + b * kTileBytes, &map_h, bar0 + 8u * b,
-                (tile % a.tiles_c) * kTile, (a.tr0 + tile / a.tiles_c) * kTile);
-  };
-  int pend[2] = {-1, -1};
-  if (t == 0) {
-    for (int b = 0; b < 2; ++b) {
-      const int k = blockIdx.x + b * gridDim.x;
-      if (k < num_tiles) {
-        load(k, b);
-        pend[b] = 0;
-      }
-    }
+  const int count = (num_tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+                    static_cast<int>(gridDim.x);
+  // last rows first: they are the most recently written, and still in L2
+  auto tile_of = [&](int i) { return num_tiles - 1 - static_cast<int>(blockIdx.x + i * gridDim.x); };
+  if (threadIdx.x >= kWorkThreads) {
+    ring.produce(count, [&](int i, int, uint32_t dst, uint32_t bar) {
+      const int tile = tile_of(i);
+      tma_load_2d(dst, &map_h, bar, (tile % a.tiles_c) * kTile, (a.tr0 + tile / a.tiles_c) * kTile);
+    });
+    return;
   }
-  int i = 0;
-  for (int k = blockIdx.x; k < num_tiles; k += gridDim.x, ++i) {
-    const int buf = i & 1;
-    const int tile = num_tiles - 1 - k;
+  const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TileEmit<1, false, POW2> emit(smem + NormColSmem::kEmit, a.out);
+  for (int i = 0; i < count; ++i) {
+    const int tile = tile_of(i);
     const int tr = a.tr0 + tile / a.tiles_c, tc = tile % a.tiles_c;
     const int64_t r0 = static_cast<int64_t>(tr) * kTile + rb * 8;
-    const int64_t c0 = static_cast<int64_t>(tc) * kTile + cg * 8;
-    float g[8], rs[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-    if (c0 < a.cols) load_gamma8(a.gamma, a.gamma_f32, c0, g);
+    const int64_t c0 = static_cast<int64_t>(tc) * kTile + lane * 4;
+    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rs[8];
+    if (c0 < a.cols) load_gamma4(a.gamma, a.gamma_f32, c0, g);
 #pragma unroll
     for (int p = 0; p < 8; ++p) rs[p] = r0 + p < a.rows ? __ldg(a.rstd + r0 + p) : 0.0f;
-    const bool got = mbar_wait(bar0 + 8u * buf, (i >> 1) & 1, abort_flag, kErrTimeoutTma);
-    if (!__syncthreads_and(got ? 1 : 0)) break;
-    pend[buf] = -1;
-    float y[8][8];
-    const uint16_t* in = reinterpret_cast<const uint16_t*>(smem + NormColSmem::kIn + buf * kTileBytes);
+    float y[1][8][4];
+    const uint8_t* in = ring.wait(i, 0);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      unpack8(ld16(in + (rb * 8 + p) * kTile + cg * 8), y[p]);
+      read4(in, p, y[0][p]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[p][j] = (y[p][j] * rs[p]) * g[j];
-    }
-    __syncthreads();   // the input buffer is free: fetch the tile after next
-    if (t == 0) {
-      const int next = k + 2 * gridDim.x;
-      if (next < num_tiles) {
-        load(next, buf);
-        pend[buf] = ((i >> 1) + 1) & 1;
+      for (int j = 0; j < 4; j += 2) {
+        fmul2(y[0][p][j], y[0][p][j + 1], y[0][p][j], y[0][p][j + 1], rs[p], rs[p]);
+        fmul2(y[0][p][j], y[0][p][j + 1], y[0][p][j], y[0][p][j + 1], g[j], g[j + 1]);
       }
     }
-    const TileOut o{nullptr, nullptr, a.q_t, a.s_t, a.rows_pad, a.cols, tr, tc};
-    emit_tile<false, true, POW2>(y, smem + NormColSmem::kEmit, o);
+    ring.release(i);
+    emit.step(y, tr, {tc});
   }
-  if (t == 0) drain_loads(bar0, pend, 2);
+  emit.finish();
 }
 
 // ---------------------------------------------------------------- backward

@@ -16,11 +16,28 @@
 namespace fp8bw {
 namespace layer {
 
-// 1 / (1 + exp(-x)) by the fast exponential and division: relative error about
-// (2 + |x|) * 2^-23. Below -87 the quotient is 0 (its value there is under
-// 2^-125); at -inf it is 0, so that x * sigmoid(x) is NaN as the formula says.
-__device__ __forceinline__ float sigmoid(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
+// 1 / (1 + exp(-x)) of two values by the approximate exponential and reciprocal
+// (packed arithmetic where the instruction exists): relative error about
+// (2 + |x|) * 2^-23. Results that would be subnormal are 0, so below -87 the
+// quotient is 0 (its value there is under 2^-125); at -inf it is 0, so that
+// x * sigmoid(x) is NaN as the formula says.
+__device__ __forceinline__ void sigmoid2(float x0, float x1, float& s0, float& s1) {
+  float e0, e1;
+  const float l = -1.4426950408889634f;      // -log2(e)
+  fmul2(x0, x1, x0, x1, l, l);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(x0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(x1));
+  fadd2(e0, e1, e0, e1, 1.0f, 1.0f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(e0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(e1));
+}
+
+// y = gate * up * sigmoid(gate), two elements.
+__device__ __forceinline__ void glu2(const float* g, const float* u, float* y) {
+  float s0, s1, w0, w1;
+  sigmoid2(g[0], g[1], s0, s1);
+  fmul2(w0, w1, u[0], u[1], g[0], g[1]);
+  fmul2(y[0], y[1], w0, w1, s0, s1);
 }
 
 // ---------------------------------------------------------------- row-wise only
@@ -52,133 +69,117 @@ __global__ void __launch_bounds__(kGluRowThreads) swiglu_row_kernel(const GluRow
     unpack8(wg, g);
     unpack8(wu, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = g[j] * sigmoid(g[j]) * u[j];
+    for (int j = 0; j < 8; j += 2) glu2(g + j, u + j, y + j);
   }
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(y[j]));
+  float m = max3_abs(max3_abs(0.0f, y[0], y[1]), y[2], y[3]);
+  m = max3_abs(max3_abs(m, y[4], y[5]), y[6], y[7]);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float qs, s;
   scale_of<POW2>(m, qs, s);
   if (row < a.rows_pad && c < a.f) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= qs;
-    *reinterpret_cast<uint2*>(a.q + row * a.f + c) = encode8(y);
+    *reinterpret_cast<uint2*>(a.q + row * a.f + c) =
+        make_uint2(encode4(y[0], y[1], y[2], y[3], qs), encode4(y[4], y[5], y[6], y[7], qs));
     if ((threadIdx.x & 15) == 0) a.s[static_cast<int64_t>(blockIdx.y) * a.rows_pad + row] = s;
   }
 }
 
 // ---------------------------------------------------------------- 128x128 tiles
 struct GluTileArgs {
-  int64_t rows_pad, f;
-  int tiles_r, tiles_c;     // of [rows_pad, f]
-  uint8_t* q;
-  float* s;
-  uint8_t* q_t;
-  float* s_t;
+  int tiles_r, tiles_c;     // of the inputs' [rows, f]
+  CodesOut out;
 };
 
-// Forward: the gate and up tiles arrive by TMA in one buffer, which is
-// refilled as soon as the products are in registers; two CTAs per SM keep
-// loads in flight through each other's encoding.
+// The block's tiles: blockIdx.x, blockIdx.x + gridDim.x, ...
+__device__ __forceinline__ int tiles_of_block(int num_tiles) {
+  return (num_tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+         static_cast<int>(gridDim.x);
+}
+
+using GluFwdRing = TileRing<2, 6>;      // gate, up
 struct GluFwdSmem {
-  static constexpr int kIn = 0;                       // gate, up
-  static constexpr int kEmit = 2 * kTileBytes;
-  static constexpr int kBar = kEmit + TileEmit::kBytes;
-  static constexpr int kBytes = kBar + 32;
-  static constexpr int kAlloc = kBytes + 128;
+  static constexpr int kEmit = (GluFwdRing::kBytes + 127) / 128 * 128;
+  static constexpr int kAlloc = kEmit + TileEmit<1, true, false>::kBytes + 128;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_tile_kernel(const __grid_constant__ CUtensorMap map_g,
                        const __grid_constant__ CUtensorMap map_u, const GluTileArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar = sbase + GluFwdSmem::kBar;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + GluFwdSmem::kBar + 16);
-  const int t = threadIdx.x, rb = t >> 4, cg = t & 15;
-  const int num_tiles = a.tiles_r * a.tiles_c;
-  if (t == 0) {
-    mbar_init(bar, 1);
-    *abort_flag = 0u;
-    fence_mbar_init();
+  const GluFwdRing ring(smem);
+  if (threadIdx.x == 0) {
+    ring.init();
     prefetch_tmap(&map_g);
     prefetch_tmap(&map_u);
   }
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  auto load = [&](int tile) {
-    const int x = (tile % a.tiles_c) * kTile, y = (tile / a.tiles_c) * kTile;
-    mbar_arrive_expect_tx(bar, 2 * kTileBytes);
-    tma_load_2d(sbase + GluFwdSmem::kIn, &map_g, bar, x, y);
-    tma_load_2d(sbase + GluFwdSmem::kIn + kTileBytes, &map_u, bar, x, y);
-  };
-  int pend[1] = {-1};
-  if (t == 0 && blockIdx.x < num_tiles) {
-    load(blockIdx.x);
-    pend[0] = 0;
+  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
+  if (threadIdx.x >= kWorkThreads) {
+    ring.produce(count, [&](int i, int n, uint32_t dst, uint32_t bar) {
+      const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
+      tma_load_2d(dst, n == 0 ? &map_g : &map_u, bar, (tile % a.tiles_c) * kTile,
+                  (tile / a.tiles_c) * kTile);
+    });
+    return;
   }
-  int i = 0;
-  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
-    const bool got = mbar_wait(bar, i & 1, abort_flag, kErrTimeoutTma);
-    if (!__syncthreads_and(got ? 1 : 0)) break;
-    pend[0] = -1;
-    float y[8][8];
-    const uint16_t* in = reinterpret_cast<const uint16_t*>(smem + GluFwdSmem::kIn);
+  TileEmit<1, true, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
+  for (int i = 0; i < count; ++i) {
+    const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
+    float y[1][8][4];
+    const uint8_t* gate = ring.wait(i, 0);
+    const uint8_t* up = ring.wait(i, 1);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      const int at = (rb * 8 + p) * kTile + cg * 8;
-      float g[8], u[8];
-      unpack8(ld16(in + at), g);
-      unpack8(ld16(in + kTile * kTile + at), u);
+      float g[4], u[4];
+      read4(gate, p, g);
+      read4(up, p, u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[p][j] = g[j] * sigmoid(g[j]) * u[j];
+      for (int j = 0; j < 4; j += 2) glu2(g + j, u + j, &y[0][p][j]);
     }
-    __syncthreads();   // the buffer is free
-    if (t == 0 && tile + gridDim.x < num_tiles) {
-      load(tile + gridDim.x);
-      pend[0] = (i + 1) & 1;
-    }
-    const TileOut o{a.q, a.s, a.q_t, a.s_t, a.rows_pad, a.f, tile / a.tiles_c, tile % a.tiles_c};
-    emit_tile<true, true, POW2>(y, smem + GluFwdSmem::kEmit, o);
+    ring.release(i);
+    emit.step(y, tile / a.tiles_c, {tile % a.tiles_c});
   }
-  if (t == 0) drain_loads(bar, pend, 1);
+  emit.finish();
+}
+
+// Two elements of the backward pass.
+__device__ __forceinline__ void glu_grad2(const float* g, const float* u, const float* d,
+                                          float* dgate, float* dup) {
+  float s0, s1, w0, w1, c0 = 1.0f, c1 = 1.0f;
+  sigmoid2(g[0], g[1], s0, s1);
+  fmul2(w0, w1, d[0], d[1], s0, s1);
+  fmul2(dup[0], dup[1], w0, w1, g[0], g[1]);
+  fmul2(w0, w1, w0, w1, u[0], u[1]);
+  ffma2(c0, c1, s0, s1, -1.0f, -1.0f);          // 1 - sg
+  float t0 = 1.0f, t1 = 1.0f;
+  ffma2(t0, t1, g[0], g[1], c0, c1);            // 1 + gate (1 - sg)
+  fmul2(dgate[0], dgate[1], w0, w1, t0, t1);
 }
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
-// two halves): gate, up and da tiles in; two output tiles (dgate, dup). Each
-// thread computes both gradients of its 8x8 sub-block at once and parks dup,
-// in fp32, in the shared memory its own gate and up values came from (the same
-// 256 bytes), so exp is evaluated once and registers hold one tile.
+// two halves): gate, up and da tiles in, a dgate and a dup tile out.
+using GluBwdRing = TileRing<3, 5>;
 struct GluBwdSmem {
-  static constexpr int kIn = 0;                       // gate, up, da
-  static constexpr int kEmit = 3 * kTileBytes - 16 * 1024;  // T overlays da's second half
-  static constexpr int kBar = kEmit + TileEmit::kBytes;
-  static constexpr int kBytes = kBar + 32;
-  static constexpr int kAlloc = kBytes + 128;
+  static constexpr int kEmit = (GluBwdRing::kBytes + 127) / 128 * 128;
+  static constexpr int kAlloc = kEmit + TileEmit<2, true, false>::kBytes + 128;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
-static_assert(TileEmit::kT == 0 && kTile * kTile == 16 * 1024, "T overlays half of the da tile");
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_bwd_tile_kernel(const __grid_constant__ CUtensorMap map_g,
                            const __grid_constant__ CUtensorMap map_u,
                            const __grid_constant__ CUtensorMap map_da, const GluTileArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar = sbase + GluBwdSmem::kBar;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + GluBwdSmem::kBar + 16);
-  const int t = threadIdx.x, rb = t >> 4, cg = t & 15;
-  const int num_tiles = a.tiles_r * a.tiles_c;
-  if (t == 0) {
-    mbar_init(bar, 1);
-    *abort_flag = 0u;
-    fence_mbar_init();
+  const GluBwdRing ring(smem);
+  if (threadIdx.x == 0) {
+    ring.init();
     prefetch_tmap(&map_g);
     prefetch_tmap(&map_u);
     prefetch_tmap(&map_da);
@@ -186,107 +187,91 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  int i = 0;
-  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
-    const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
-    if (t == 0) {
-      mbar_arrive_expect_tx(bar, 3 * kTileBytes);
-      tma_load_2d(sbase, &map_g, bar, tc * kTile, tr * kTile);
-      tma_load_2d(sbase + kTileBytes, &map_u, bar, tc * kTile, tr * kTile);
-      tma_load_2d(sbase + 2 * kTileBytes, &map_da, bar, tc * kTile, tr * kTile);
-    }
-    const bool got = mbar_wait(bar, i & 1, abort_flag, kErrTimeoutTma);
-    if (!__syncthreads_and(got ? 1 : 0)) {
-      if (t == 0) {
-        const int pend[1] = {i & 1};
-        drain_loads(bar, pend, 1);
-      }
-      break;
-    }
-    float y[8][8];
-    uint8_t* in = smem;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int at = ((rb * 8 + p) * kTile + cg * 8) * 2;
-      float g[8], u[8], d[8];
-      unpack8(ld16(in + at), g);
-      unpack8(ld16(in + kTileBytes + at), u);
-      unpack8(ld16(in + 2 * kTileBytes + at), d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float sg = sigmoid(g[j]);
-        const float w = d[j] * sg;
-        y[p][j] = w * u[j] * fmaf(g[j], 1.0f - sg, 1.0f);
-        u[j] = w * g[j];
-      }
-      *reinterpret_cast<float4*>(in + at) = make_float4(u[0], u[1], u[2], u[3]);
-      *reinterpret_cast<float4*>(in + kTileBytes + at) = make_float4(u[4], u[5], u[6], u[7]);
-    }
-    __syncthreads();   // da's buffer is free: it holds the transposed codes now
-    TileOut o{a.q, a.s, a.q_t, a.s_t, a.rows_pad, 2 * a.f, tr, tc};
-    emit_tile<true, true, POW2>(y, smem + GluBwdSmem::kEmit, o);
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int at = ((rb * 8 + p) * kTile + cg * 8) * 2;
-      const float4 lo = *reinterpret_cast<const float4*>(in + at);
-      const float4 hi = *reinterpret_cast<const float4*>(in + kTileBytes + at);
-      y[p][0] = lo.x, y[p][1] = lo.y, y[p][2] = lo.z, y[p][3] = lo.w;
-      y[p][4] = hi.x, y[p][5] = hi.y, y[p][6] = hi.z, y[p][7] = hi.w;
-    }
-    o.tc = tc + a.tiles_c;
-    emit_tile<true, true, POW2, true>(y, smem + GluBwdSmem::kEmit, o);
+  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
+  if (threadIdx.x >= kWorkThreads) {
+    ring.produce(count, [&](int i, int n, uint32_t dst, uint32_t bar) {
+      const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
+      tma_load_2d(dst, n == 0 ? &map_g : n == 1 ? &map_u : &map_da, bar,
+                  (tile % a.tiles_c) * kTile, (tile / a.tiles_c) * kTile);
+    });
+    return;
   }
+  TileEmit<2, true, POW2> emit(smem + GluBwdSmem::kEmit, a.out);
+  for (int i = 0; i < count; ++i) {
+    const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
+    const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
+    float y[2][8][4];
+    const uint8_t* gate = ring.wait(i, 0);
+    const uint8_t* up = ring.wait(i, 1);
+    const uint8_t* da = ring.wait(i, 2);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float g[4], u[4], d[4];
+      read4(gate, p, g);
+      read4(up, p, u);
+      read4(da, p, d);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) glu_grad2(g + j, u + j, d + j, &y[0][p][j], &y[1][p][j]);
+    }
+    ring.release(i);
+    emit.step(y, tr, {tc, tc + a.tiles_c});
+  }
+  emit.finish();
 }
 
 // Backward for f no multiple of 128: the 1x128 groups of d then straddle the
 // dgate/dup boundary, so each tile of d's 2f columns is computed by itself,
-// every 8-column run from its own gate, up and da columns (read twice in all,
+// every 4-column run from its own gate, up and da columns (read twice in all,
 // with plain loads).
 struct GluRaggedArgs {
   const uint16_t* gu;
   const uint16_t* da;
-  int64_t rows;
-  GluTileArgs t;            // tiles of [rows_pad, 2f]
+  int64_t rows, f;
+  GluTileArgs t;            // tiles of the output's [rows, 2f]
 };
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kWorkThreads, 2)
     swiglu_bwd_ragged_kernel(const GluRaggedArgs r) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
   const GluTileArgs& a = r.t;
-  const int t = threadIdx.x, rb = t >> 4, cg = t & 15;
+  const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int num_tiles = a.tiles_r * a.tiles_c;
   launch_dependents();
   grid_dependency_wait();
+  TileEmit<1, true, POW2> emit(smem, a.out);
   for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
     const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
-    const int64_t c0 = static_cast<int64_t>(tc) * kTile + cg * 8;
-    const bool is_up = c0 >= a.f;
-    const int64_t src = is_up ? c0 - a.f : c0;
-    float y[8][8];
+    const int64_t c0 = static_cast<int64_t>(tc) * kTile + lane * 4;
+    const bool is_up = c0 >= r.f;
+    const int64_t src = is_up ? c0 - r.f : c0;
+    float y[1][8][4];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int64_t row = static_cast<int64_t>(tr) * kTile + rb * 8 + p;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[p][j] = 0.0f;
-      if (row < r.rows && c0 < 2 * a.f) {
-        const uint16_t* gp = r.gu + row * 2 * a.f + src;
-        float g[8], u[8], d[8];
-        unpack8(ld16(gp), g);
-        unpack8(ld16(gp + a.f), u);
-        unpack8(ld16(r.da + row * a.f + src), d);
+      for (int j = 0; j < 4; ++j) y[0][p][j] = 0.0f;
+      if (row < r.rows && c0 < 2 * r.f) {
+        const uint16_t* gp = r.gu + row * 2 * r.f + src;
+        const uint2 wg = *reinterpret_cast<const uint2*>(gp);
+        const uint2 wu = *reinterpret_cast<const uint2*>(gp + r.f);
+        const uint2 wd = *reinterpret_cast<const uint2*>(r.da + row * r.f + src);
+        const float g[4] = {bf16_lo(wg.x), bf16_hi(wg.x), bf16_lo(wg.y), bf16_hi(wg.y)};
+        const float u[4] = {bf16_lo(wu.x), bf16_hi(wu.x), bf16_lo(wu.y), bf16_hi(wu.y)};
+        const float d[4] = {bf16_lo(wd.x), bf16_hi(wd.x), bf16_lo(wd.y), bf16_hi(wd.y)};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float sg = sigmoid(g[j]);
-          const float w = d[j] * sg;
-          y[p][j] = is_up ? w * g[j] : w * u[j] * fmaf(g[j], 1.0f - sg, 1.0f);
+        for (int j = 0; j < 4; j += 2) {
+          float dgate[2], dup[2];
+          glu_grad2(g + j, u + j, d + j, dgate, dup);
+          y[0][p][j] = is_up ? dup[0] : dgate[0];
+          y[0][p][j + 1] = is_up ? dup[1] : dgate[1];
         }
       }
     }
-    const TileOut o{a.q, a.s, a.q_t, a.s_t, a.rows_pad, 2 * a.f, tr, tc};
-    emit_tile<true, true, POW2>(y, smem, o);
+    emit.step(y, tr, {tc});
   }
+  emit.finish();
 }
 
 }  // namespace layer

@@ -1,8 +1,13 @@
 // tile_quant.cuh -- E4M3 quantisation of 128x128 tiles of fp32 values that a
 // kernel holds in registers: row-wise codes with 1x128 scales and/or
 // column-wise codes (transposed) with 128x1 scales, with the arithmetic and
-// layouts of the quantisers. 256 threads; thread t owns the 8x8 sub-block of
-// rows 8*(t/16) .. +7 and columns 8*(t%16) .. +7.
+// layouts of the quantisers.
+//
+// 512 working threads: warp w owns rows 8w .. 8w+7 of the tile and lane l the
+// columns 4l .. 4l+3, so a warp holds eight whole 1x128 groups and a thread 32
+// values per tile (two tiles at once fit its registers). A 17th warp only loads:
+// it keeps a ring of input tiles filled by TMA, so reads stay in flight while
+// the others work.
 #pragma once
 
 #include <cuda.h>
@@ -13,7 +18,8 @@ namespace fp8bw {
 namespace layer {
 
 constexpr int kTile = 128;
-constexpr int kTileThreads = 256;
+constexpr int kWorkThreads = 512;
+constexpr int kTileThreads = kWorkThreads + 32;
 constexpr int kTileBytes = kTile * kTile * 2;   // one bf16 tile
 
 __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
@@ -21,158 +27,296 @@ __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
                                     ~static_cast<uintptr_t>(127));
 }
 
-// Encode 8 values (already multiplied by qscale) into 8 bytes.
-__device__ __forceinline__ uint2 encode8(const float (&t)[8]) {
-  return make_uint2(e4m3x2(t[0], t[1]) | (e4m3x2(t[2], t[3]) << 16),
-                    e4m3x2(t[4], t[5]) | (e4m3x2(t[6], t[7]) << 16));
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Shared memory of emit_tile.
-struct TileEmit {
-  static constexpr int kT = 0;                          // transposed codes, 16 KB
-  static constexpr int kRed = kT + kTile * kTile;       // 8 x 128 floats
-  static constexpr int kColQ = kRed + 8 * kTile * 4;    // 128 floats
-  static constexpr int kSRow = kColQ + kTile * 4;       // 128 floats
-  static constexpr int kBytes = kSRow + kTile * 4;
+// Four values as E4M3 (round to nearest even, saturating), a in the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Four values times k, as E4M3.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float k) {
+  fmul2(a, b, a, b, k, k);
+  fmul2(c, d, c, d, k, k);
+  return e4m3x4(a, b, c, d);
+}
+
+// max(m, |a|, |b|) in one instruction.
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+
+// Largest |v| of the warp, in every lane.
+__device__ __forceinline__ float warp_max_abs(float v) {
+  float r;
+  asm volatile("redux.sync.max.abs.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ void fadd2(float& p0, float& p1, float x0, float x1, float y0,
+                                      float y1) {
+  asm("{\n\t.reg .b64 p, x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 p, x, y;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(p0), "=f"(p1)
+      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
+
+// A barrier of the working threads.
+__device__ __forceinline__ void work_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kWorkThreads) : "memory");
+}
+
+// Where codes and scales go (row-wise ones may be unused).
+struct CodesOut {
+  uint8_t* q;          // [rows][cols]
+  float* s;            // [ceil(cols/128)][rows]
+  uint8_t* q_t;        // [cols][rows]
+  float* s_t;          // [ceil(rows/128)][cols]
+  int64_t rows, cols;  // rows padded to a multiple of 16; cols is one too
 };
 
-// Where a tile's codes and scales go (row-wise or column-wise may be unused).
-struct TileOut {
-  uint8_t* q;          // [rows_pad][cols]
-  float* s;            // [ceil(cols/128)][rows_pad]
-  uint8_t* q_t;        // [cols][rows_pad]
-  float* s_t;          // [ceil(rows_pad/128)][cols]
-  int64_t rows, cols;  // rows = rows_pad, a multiple of 16; cols too
-  int tr, tc;          // tile coordinates
-};
-
-// Byte offset in the transposed tile of the 8-byte unit of tokens 8u .. 8u+7
-// of column k; units are xor-ed with the column block, so the 16 column blocks
-// of a half-warp hit 16 different bank pairs.
+// Byte offset in a transposed tile of the 8-byte unit of tokens 8u .. 8u+7 of
+// column k. Units are xor-ed with the 4-column block (the 32 columns that a
+// warp writes at once, 4 apart, land in all 16 bank pairs) and with the column's
+// parity (the four columns that it reads at once use even and odd units).
 __device__ __forceinline__ int emit_t_offset(int k, int u) {
-  return k * kTile + ((u ^ (k >> 3)) & 15) * 8;
+  return k * kTile + ((u ^ (k >> 2) ^ (k & 1)) & 15) * 8;
 }
 
-// All 256 threads call this with their 8x8 values; entries outside the tensor
-// must be zero. Begins with the shared memory free (all threads past the
-// previous use) and ends with a barrier after the last use.
-// FENCE: the shared memory this block has written is about to be overwritten
-// by bulk copies (issued after that barrier).
-template <bool ROW, bool COL, bool POW2, bool FENCE = false>
-__device__ __forceinline__ void emit_tile(const float (&y)[8][8], uint8_t* smem,
-                                          const TileOut& o) {
-  uint8_t* T = smem + TileEmit::kT;
-  float(*red)[kTile] = reinterpret_cast<float(*)[kTile]>(smem + TileEmit::kRed);
-  float* colq = reinterpret_cast<float*>(smem + TileEmit::kColQ);
-  float* srow = reinterpret_cast<float*>(smem + TileEmit::kSRow);
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rb = t >> 4, cg = t & 15;
-  const int64_t r0 = static_cast<int64_t>(o.tr) * kTile + rb * 8;
-  const int64_t c0 = static_cast<int64_t>(o.tc) * kTile + cg * 8;
-  const bool valid = r0 < o.rows && c0 < o.cols;
+// Writes the codes of NOUT tiles per step, all of row tile tr, from the 8x4
+// values of each working thread; entries outside the tensor must be zero. Column
+// scales need the whole tile, so a step has two barriers. To have work between
+// them, the transposed codes of a step leave shared memory during the next one:
+// between the barriers lie this step's row codes, the last step's transposed
+// codes and (in a few warps) the column scales.
+template <int NOUT, bool ROW, bool POW2>
+struct TileEmit {
+  static constexpr int kT = 0;                                   // NOUT x 16 KB
+  static constexpr int kRed = kT + NOUT * kTile * kTile;         // NOUT x 16 x 128 floats
+  static constexpr int kColQ = kRed + NOUT * 16 * kTile * 4;     // NOUT x 128 floats
+  static constexpr int kBytes = kColQ + NOUT * kTile * 4;
 
-  if constexpr (COL) {
-    // column maxima: 8 rows here, x2 across the half-warps, x8 warps below
-    float cm[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      cm[j] = fabsf(y[0][j]);
-#pragma unroll
-      for (int p = 1; p < 8; ++p) cm[j] = fmaxf(cm[j], fabsf(y[p][j]));
-      cm[j] = fmaxf(cm[j], __shfl_xor_sync(0xFFFFFFFFu, cm[j], 16));
-    }
-    if (lane < 16) {
-      float4* dst = reinterpret_cast<float4*>(&red[warp][cg * 8]);
-      dst[0] = make_float4(cm[0], cm[1], cm[2], cm[3]);
-      dst[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
-    }
+  uint8_t* smem;
+  const CodesOut& out;
+  int64_t row_at, col_at;      // this thread's offsets in a tile of q and q_t
+  int last_tr = -1, last_tc[NOUT];
+
+  __device__ __forceinline__ TileEmit(uint8_t* p, const CodesOut& o) : smem(p), out(o) {
+    const int t = threadIdx.x;
+    row_at = static_cast<int64_t>((t >> 5) * 8) * o.cols + (t & 31) * 4;
+    col_at = static_cast<int64_t>(t >> 3) * o.rows + (t & 7) * 16;
   }
-  if constexpr (ROW) {
-    // the 16 lanes of a half-warp share 8 rows; lane (cg & 7) computes the
-    // scale of row (cg & 7)
-    float mine = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      float m = fabsf(y[p][0]);
-#pragma unroll
-      for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(y[p][j]));
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      if ((cg & 7) == p) mine = m;
-    }
-    float qs, s;
-    scale_of<POW2>(mine, qs, s);
-    if (cg < 8) srow[rb * 8 + cg] = s;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const float k = __shfl_sync(0xFFFFFFFFu, qs, (lane & 16) | p);
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) fmul2(v[j], v[j + 1], y[p][j], y[p][j + 1], k, k);
-      if (valid) *reinterpret_cast<uint2*>(o.q + (r0 + p) * o.cols + c0) = encode8(v);
-    }
+
+  // What is left of the tensor from tile index i on, at most a tile.
+  __device__ __forceinline__ static int left(int64_t size, int i) {
+    return static_cast<int>(min(static_cast<int64_t>(kTile), size - static_cast<int64_t>(i) * kTile));
   }
-  if constexpr (COL) {
-    __syncthreads();
-    if (t < kTile) {
-      float m = red[0][t];
+
+  __device__ __forceinline__ void step(const float (&y)[NOUT][8][4], int tr, const int (&tc)[NOUT]) {
+    const int t = threadIdx.x, rb = t >> 5, lane = t & 31;
+    float* red = reinterpret_cast<float*>(smem + kRed);
+    float* colq = reinterpret_cast<float*>(smem + kColQ);
+    // column maxima of this warp's 8 rows
 #pragma unroll
-      for (int w = 1; w < kTileThreads / 32; ++w) m = fmaxf(m, red[w][t]);
+    for (int n = 0; n < NOUT; ++n) {
+      float m[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[j] = max3_abs(0.0f, y[n][0][j], y[n][1][j]);
+#pragma unroll
+        for (int p = 2; p < 8; p += 2) m[j] = max3_abs(m[j], y[n][p][j], y[n][p + 1][j]);
+      }
+      *reinterpret_cast<float4*>(red + (n * 16 + rb) * kTile + lane * 4) =
+          make_float4(m[0], m[1], m[2], m[3]);
+    }
+    work_sync();
+    if (t < NOUT * kTile) {
+      const int n = t >> 7, k = t & 127;
+      const float* r = red + n * 16 * kTile + k;
+      float m = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 16; w += 2) m = max3_abs(m, r[w * kTile], r[(w + 1) * kTile]);
       float qs, s;
       scale_of<POW2>(m, qs, s);
       colq[t] = qs;
-      const int64_t col = static_cast<int64_t>(o.tc) * kTile + t;
-      if (col < o.cols) o.s_t[static_cast<int64_t>(o.tr) * o.cols + col] = s;
+      const int c = NOUT == 1 || n == 0 ? tc[0] : tc[NOUT - 1];
+      if (k < left(out.cols, c))
+        out.s_t[static_cast<int64_t>(tr) * out.cols + static_cast<int64_t>(c) * kTile + k] = s;
     }
-    __syncthreads();
-    const float4 q0 = *reinterpret_cast<const float4*>(&colq[cg * 8]);
-    const float4 q1 = *reinterpret_cast<const float4*>(&colq[cg * 8 + 4]);
-    const float qv[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    if (last_tr >= 0) write_transposed();
+    if constexpr (ROW) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v[8];
-#pragma unroll
-      for (int p = 0; p < 8; p += 2) fmul2(v[p], v[p + 1], y[p][j], y[p + 1][j], qv[j], qv[j]);
-      *reinterpret_cast<uint2*>(T + emit_t_offset(cg * 8 + j, rb)) = encode8(v);
+      for (int n = 0; n < NOUT; ++n) write_rows(y[n], tr, tc[n]);
     }
+    work_sync();
+#pragma unroll
+    for (int n = 0; n < NOUT; ++n) {
+      uint8_t* T = smem + kT + n * kTile * kTile;
+      const float4 k4 = *reinterpret_cast<const float4*>(colq + n * kTile + lane * 4);
+      float v[8][4];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        fmul2(v[p][0], v[p][1], y[n][p][0], y[n][p][1], k4.x, k4.y);
+        fmul2(v[p][2], v[p][3], y[n][p][2], y[n][p][3], k4.z, k4.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint2*>(T + emit_t_offset(lane * 4 + j, rb)) =
+            make_uint2(e4m3x4(v[0][j], v[1][j], v[2][j], v[3][j]),
+                       e4m3x4(v[4][j], v[5][j], v[6][j], v[7][j]));
+      last_tc[n] = tc[n];
+    }
+    last_tr = tr;
   }
-  __syncthreads();
-  if constexpr (ROW) {
-    if (t < kTile / 4) {
-      const int64_t row = static_cast<int64_t>(o.tr) * kTile + t * 4;
-      if (row < o.rows)
-        *reinterpret_cast<float4*>(o.s + static_cast<int64_t>(o.tc) * o.rows + row) =
-            *reinterpret_cast<const float4*>(&srow[t * 4]);
-    }
+
+  // After the last step.
+  __device__ __forceinline__ void finish() {
+    if (last_tr < 0) return;
+    work_sync();
+    write_transposed();
   }
-  if constexpr (COL) {
-    // tile column k is 128 contiguous tokens of row tc*128 + k of q_t
+
+  __device__ __forceinline__ void write_transposed() const {
+    const int kk = threadIdx.x >> 3, ch = threadIdx.x & 7;
+    const bool rin = ch * 16 < left(out.rows, last_tr);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int idx = it * kTileThreads + t;
-      const int kk = idx >> 3, ch = idx & 7;
-      const int64_t col = static_cast<int64_t>(o.tc) * kTile + kk;
-      const int64_t tok = static_cast<int64_t>(o.tr) * kTile + ch * 16;
-      if (col < o.cols && tok < o.rows) {
-        const uint2 lo = *reinterpret_cast<const uint2*>(T + emit_t_offset(kk, 2 * ch));
-        const uint2 hi = *reinterpret_cast<const uint2*>(T + emit_t_offset(kk, 2 * ch + 1));
-        *reinterpret_cast<uint4*>(o.q_t + col * o.rows + tok) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    for (int n = 0; n < NOUT; ++n) {
+      // tile column k is 128 contiguous tokens of row tc*128 + k of q_t
+      const uint8_t* T = smem + kT + n * kTile * kTile;
+      const int cols = left(out.cols, last_tc[n]);
+      uint8_t* dst = out.q_t + static_cast<int64_t>(last_tc[n]) * kTile * out.rows +
+                     static_cast<int64_t>(last_tr) * kTile + col_at;
+#pragma unroll
+      for (int k0 = 0; k0 < kTile; k0 += kWorkThreads / 8) {
+        const uint2 lo = *reinterpret_cast<const uint2*>(T + emit_t_offset(k0 + kk, 2 * ch));
+        const uint2 hi = *reinterpret_cast<const uint2*>(T + emit_t_offset(k0 + kk, 2 * ch + 1));
+        if (rin && k0 + kk < cols)
+          *reinterpret_cast<uint4*>(dst + k0 * out.rows) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
     }
   }
-  if constexpr (FENCE) fence_proxy_async_smem();
-  __syncthreads();
-}
 
-// After an early exit: wait (bounded) for the loads still in flight before the
-// shared memory is released. pend[b]: parity of a load nobody waited for, or -1.
-__device__ __forceinline__ void drain_loads(uint32_t bar0, const int* pend, int n) {
-  for (int b = 0; b < n; ++b) {
-    if (pend[b] < 0) continue;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar0 + 8u * b, static_cast<uint32_t>(pend[b])) &&
-           globaltimer_ns() - t0 < kWaitLimitNs) {
+  __device__ __forceinline__ void write_rows(const float (&y)[8][4], int tr, int tc) const {
+    const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // row maxima; lane l computes the scale of row l & 7
+    float mine = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float m = warp_max_abs(max3_abs(max3_abs(0.0f, y[p][0], y[p][1]), y[p][2], y[p][3]));
+      if ((lane & 7) == p) mine = m;
+    }
+    float qs, s;
+    scale_of<POW2>(mine, qs, s);
+    // rows is a multiple of 16: the warp's 8 rows are all in or all out
+    const bool rin = rb * 8 < left(out.rows, tr);
+    const int64_t r0 = static_cast<int64_t>(tr) * kTile;
+    if (lane < 8 && rin) out.s[static_cast<int64_t>(tc) * out.rows + r0 + rb * 8 + lane] = s;
+    uint8_t* q = out.q + r0 * out.cols + static_cast<int64_t>(tc) * kTile + row_at;
+    const bool in = rin && lane * 4 < left(out.cols, tc);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float k = __shfl_sync(0xFFFFFFFFu, qs, p);
+      const uint32_t code = encode4(y[p][0], y[p][1], y[p][2], y[p][3], k);
+      if (in) *reinterpret_cast<uint32_t*>(q) = code;
+      q += out.cols;
     }
   }
+};
+
+// ---------------------------------------------------------------- input ring
+// A ring of SLOTS bf16 tiles, filled by the 17th warp and read by the 16 working
+// ones; the i-th step of a block takes the NIN tiles i*NIN .. i*NIN+NIN-1 of the
+// sequence. Every wait is bounded. After an expired one the working warps go on
+// through their remaining steps (the abort flag ends every further wait), so
+// that all of them meet at every barrier.
+template <int NIN, int SLOTS>
+struct TileRing {
+  static constexpr int kBar = SLOTS * kTileBytes;            // full, empty
+  static constexpr int kBytes = kBar + 2 * SLOTS * 8 + 16;
+
+  uint8_t* base;
+  uint32_t bar;
+  volatile uint32_t* abort;
+
+  __device__ __forceinline__ explicit TileRing(uint8_t* p)
+      : base(p), bar(smem_u32(p) + kBar),
+        abort(reinterpret_cast<volatile uint32_t*>(p + kBar + 2 * SLOTS * 8)) {}
+  __device__ __forceinline__ uint32_t full(int s) const { return bar + 8u * s; }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bar + 8u * (SLOTS + s); }
+  __device__ __forceinline__ void init() const {      // one thread
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kWorkThreads / 32);
+    }
+    *abort = 0u;
+    fence_mbar_init();
+  }
+  // The loading warp: `fill(i, n, dst, bar)` issues the load of the n-th input
+  // of step i, for i in [0, steps).
+  template <typename Fill>
+  __device__ __forceinline__ void produce(int steps, Fill&& fill) const {
+    if ((threadIdx.x & 31) != 0) return;
+    const int total = steps * NIN;
+    int i = 0;
+    for (; i < total; ++i) {
+      const int s = i % SLOTS;
+      if (!mbar_wait(empty(s), ((i / SLOTS) & 1) ^ 1, abort, kErrTimeoutTma)) break;
+      mbar_arrive_expect_tx(full(s), kTileBytes);
+      fill(i / NIN, i % NIN, smem_u32(base) + s * kTileBytes, full(s));
+    }
+    // the block's shared memory must outlive the copies into it: wait for the
+    // last ones even if their readers have given up
+    for (int k = i > SLOTS ? i - SLOTS : 0; k < i; ++k) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(full(k % SLOTS), (k / SLOTS) & 1) &&
+             globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  }
+  // The working warps: wait for input n of step i (nullptr after an expired
+  // wait); release it once it has been read.
+  __device__ __forceinline__ const uint8_t* wait(int i, int n) const {
+    const int k = i * NIN + n;
+    return mbar_wait(full(k % SLOTS), (k / SLOTS) & 1, abort, kErrTimeoutTma)
+               ? base + (k % SLOTS) * kTileBytes
+               : nullptr;
+  }
+  __device__ __forceinline__ void release(int i) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int n = 0; n < NIN; ++n) mbar_arrive(empty((i * NIN + n) % SLOTS));
+    }
+  }
+};
+
+// This thread's four values of row p of its 8x4 block (zeros without a tile).
+__device__ __forceinline__ void read4(const uint8_t* tile, int p, float (&f)[4]) {
+  if (tile == nullptr) {
+    f[0] = f[1] = f[2] = f[3] = 0.0f;
+    return;
+  }
+  const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint2 w = *reinterpret_cast<const uint2*>(tile + (rb * 8 + p) * (kTile * 2) + lane * 8);
+  f[0] = bf16_lo(w.x);
+  f[1] = bf16_hi(w.x);
+  f[2] = bf16_lo(w.y);
+  f[3] = bf16_hi(w.y);
 }
 
 }  // namespace layer
