@@ -1,13 +1,17 @@
-"""Build the CUDA library libfp8bw.so in-tree for sm_100a (nvcc, no torch).
+"""Build the CUDA library libfp8bw.so in-tree for sm_100a (nvcc, no torch), and
+its Python binding.
 
 Two translation units, each including its kernel headers: csrc/api.cu (the
 quantisers and GEMMs) and csrc/layer/layer.cu (the operators around them);
 cudart is linked statically; the driver's TMA encoder is reached through
-cudaGetDriverEntryPoint, so no libcuda link is needed at build time.
+cudaGetDriverEntryPoint, so no libcuda link is needed at build time. Besides,
+one CPython extension module (csrc/layer/binding.cpp, host code) that gives the
+layer operators' Python calls a short path.
 """
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -31,6 +35,40 @@ def _sources():
     return srcs + [HEADER, LAYER_HEADER]
 
 
+# The Python binding of the layer operators: a CPython extension module, host
+# code only, compiled against the installed torch.
+BINDING_SRC = os.path.join(CSRC, "layer", "binding.cpp")
+BINDING = os.path.join(HERE, "_layer_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def _binding_stale() -> bool:
+    return not os.path.exists(BINDING) or \
+        os.path.getmtime(BINDING_SRC) > os.path.getmtime(BINDING)
+
+
+def build_binding(force: bool = False) -> str:
+    if not force and not _binding_stale():
+        return BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I" + os.path.join(root, "include"),
+           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+           "-o", tmp, BINDING_SRC, "-L" + lib, "-Wl,-rpath," + lib,
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building the layer operators' binding")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _nvcc():
     for cand in (os.environ.get("NVCC"), "/usr/local/cuda/bin/nvcc", "nvcc"):
         if cand and (os.path.isabs(cand) and os.path.exists(cand) or
@@ -40,6 +78,10 @@ def _nvcc():
 
 
 def needs_build() -> bool:
+    return _lib_stale() or _binding_stale()
+
+
+def _lib_stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
@@ -47,7 +89,8 @@ def needs_build() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not needs_build():
+    build_binding(force)
+    if not force and not _lib_stale():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [_nvcc()] + NVCC_FLAGS + ["-o", tmp] + UNITS

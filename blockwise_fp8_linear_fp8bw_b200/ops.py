@@ -26,6 +26,19 @@ FP8BW_ERR_SCALE = -9
 
 _lib = _native.load()
 
+from . import _layer_binding as _fast  # noqa: E402  (built by load() if missing)
+
+
+def _bind(lib):
+    _fast.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "fp8bw_rmsnorm_quantize", "fp8bw_rmsnorm_quantize_pow2",
+        "fp8bw_rmsnorm_backward_workspace", "fp8bw_rmsnorm_backward",
+        "fp8bw_swiglu_quantize", "fp8bw_swiglu_quantize_pow2",
+        "fp8bw_swiglu_backward_quantize", "fp8bw_swiglu_backward_quantize_pow2")))
+
+
+_bind(_lib)
+
 
 class Fp8bwError(RuntimeError):
     def __init__(self, status: int, call: str):
@@ -381,40 +394,6 @@ def _pad16(rows):
     return (rows + 15) // 16 * 16
 
 
-def _input(t, dtype, shape, name, dev):
-    """Device pointer of a contiguous input of that dtype and shape on `dev`."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError("%s: expected %s %s, got %s %s" %
-                         (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    if t.device != dev:
-        raise ValueError("expected tensors on one CUDA device, got %s and %s"
-                         % (dev, t.device))
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _need_cuda(dev):
-    if dev.type != "cuda":
-        raise ValueError("expected a CUDA tensor")
-
-
-def _run(name, dev, stream, *args):
-    """_call for the allocating helpers below, whose tensors are known to be on
-    `dev` (their calls can be a few microseconds long, most of which would be
-    the checks of buffers that were just allocated)."""
-    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None \
-        else _stream(stream, dev)
-    fn = getattr(_lib, name)
-    if dev.index == torch._C._cuda_getDevice():
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, handle)
-    if status != FP8BW_OK:
-        _check(status, name)
-
-
 def _gamma_is_f32(gamma, cols):
     if gamma.dtype not in (torch.bfloat16, torch.float32) or \
             tuple(gamma.shape) != (cols,):
@@ -599,101 +578,57 @@ class NormCodes(NamedTuple):
     rstd: torch.Tensor
 
 
-def _empty_codes(rows, cols, dev, colwise):
-    """Codes' buffers and their device pointers."""
-    rp = _pad16(rows)
-    q = torch.empty((rp, cols), dtype=torch.uint8, device=dev)
-    s = torch.empty((_cdiv(cols, 128), rp), dtype=torch.float32, device=dev)
-    if not colwise:
-        return (q, s, None, None), (q.data_ptr(), s.data_ptr(), None, None)
-    q_t = torch.empty((cols, rp), dtype=torch.uint8, device=dev)
-    s_t = torch.empty((_cdiv(rp, 128), cols), dtype=torch.float32, device=dev)
-    return (q, s, q_t, s_t), (q.data_ptr(), s.data_ptr(), q_t.data_ptr(),
-                              s_t.data_ptr())
-
-
-def _norm_inputs(x, gamma, residual):
-    _expect_2d(x, torch.bfloat16, "x")
-    dev, shape = x.device, x.shape
-    is_f32 = _gamma_is_f32(gamma, shape[1])
-    return (dev, shape, is_f32, _input(x, torch.bfloat16, shape, "x", dev),
-            _input(gamma, gamma.dtype, gamma.shape, "gamma", dev),
-            None if residual is None else
-            _input(residual, torch.bfloat16, shape, "residual", dev))
+def _fast_call(fn, name, like, stream, *args):
+    """Call `fn` of the native binding (checks, allocation and launch on the
+    current stream of the tensors' device) with `stream` current."""
+    if stream is None:
+        r = fn(*args)
+    else:
+        dev = like.device
+        if not like.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        _stream(stream, dev)            # refuses another device's stream
+        with _allocating(stream, dev):
+            r = fn(*args)
+    if r[0] != FP8BW_OK:
+        _check(r[0], name)
+    return r[1:]
 
 
 def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, colwise=False,
                      stream=None, pow2=False):
     """-> NormCodes of the root-mean-square norm of x (+ residual) times
     gamma; h is the bf16 sum (x itself without a residual)."""
-    dev, (rows, cols), is_f32, px, pg, pr = _norm_inputs(x, gamma, residual)
-    _need_cuda(dev)
-    with _allocating(stream, dev):
-        h = x if pr is None else torch.empty_like(x)
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-        codes, ptrs = _empty_codes(rows, cols, dev, colwise)
-    _run(_fn("fp8bw_rmsnorm_quantize", pow2), dev, stream, px, pr, pg, is_f32,
-         rows, cols, eps, None if pr is None else h.data_ptr(),
-         rstd.data_ptr(), None, *ptrs)
-    return NormCodes(*codes, h, rstd)
+    return NormCodes._make(_fast_call(
+        _fast.rmsnorm, "fp8bw_rmsnorm_quantize", x, stream, x, gamma, residual,
+        eps, True, colwise, pow2))
 
 
 def rmsnorm(x, gamma, residual=None, eps=1e-6, stream=None):
     """-> (y, h, rstd): the norm's bf16 output without quantisation (for what
     is not an FP8 linear: a final norm, a router)."""
-    dev, (rows, cols), is_f32, px, pg, pr = _norm_inputs(x, gamma, residual)
-    _need_cuda(dev)
-    with _allocating(stream, dev):
-        h = x if pr is None else torch.empty_like(x)
-        y = torch.empty_like(x)
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-    _run("fp8bw_rmsnorm_quantize", dev, stream, px, pr, pg, is_f32, rows, cols,
-         eps, None if pr is None else h.data_ptr(), rstd.data_ptr(),
-         y.data_ptr(), None, None, None, None)
-    return y, h, rstd
+    return _fast_call(_fast.rmsnorm, "fp8bw_rmsnorm_quantize", x, stream, x,
+                      gamma, residual, eps, False, False, False)
 
 
 def rmsnorm_backward(dy, h, rstd, gamma, dres=None, stream=None):
     """-> (dh, dgamma): the gradient of x (and of the residual), bf16, and the
     fp32 gradient of gamma. `dres` is the gradient that reaches h directly."""
-    dev, (rows, cols), is_f32, ph, pg, pr = _norm_inputs(h, gamma, dres)
-    pdy = _input(dy, torch.bfloat16, h.shape, "dy", dev)
-    ps = _input(rstd, torch.float32, (rows,), "rstd", dev)
-    _need_cuda(dev)
-    size = rmsnorm_backward_workspace(rows, cols)
-    with _allocating(stream, dev):
-        dh = torch.empty_like(h)
-        dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
-        ws = torch.empty((size,), dtype=torch.uint8, device=dev)
-    _run("fp8bw_rmsnorm_backward", dev, stream, pdy, ph, ps, pg, is_f32, pr,
-         rows, cols, dh.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), size)
-    return dh, dgamma
+    return _fast_call(_fast.rmsnorm_backward, "fp8bw_rmsnorm_backward", h,
+                      stream, dy, h, rstd, gamma, dres)
 
 
 def swiglu_quantize(gu, colwise=False, stream=None, pow2=False):
     """-> Codes of silu(gate) * up, gu = [gate | up] ([rows, 2f])."""
-    rows, f = _glu_shape(gu)
-    dev = gu.device
-    pg = _input(gu, torch.bfloat16, gu.shape, "gu", dev)
-    _need_cuda(dev)
-    with _allocating(stream, dev):
-        codes, ptrs = _empty_codes(rows, f, dev, colwise)
-    _run(_fn("fp8bw_swiglu_quantize", pow2), dev, stream, pg, rows, f, *ptrs)
-    return Codes(*codes)
+    return Codes._make(_fast_call(_fast.swiglu, "fp8bw_swiglu_quantize", gu,
+                                  stream, gu, colwise, pow2))
 
 
 def swiglu_backward_quantize(da, gu, stream=None, pow2=False):
     """-> Codes (both ways) of [dgate | dup] ([rows, 2f])."""
-    rows, f = _glu_shape(gu)
-    dev = gu.device
-    pg = _input(gu, torch.bfloat16, gu.shape, "gu", dev)
-    pd = _input(da, torch.bfloat16, (rows, f), "da", dev)
-    _need_cuda(dev)
-    with _allocating(stream, dev):
-        codes, ptrs = _empty_codes(rows, 2 * f, dev, True)
-    _run(_fn("fp8bw_swiglu_backward_quantize", pow2), dev, stream, pd, pg,
-         rows, f, *ptrs)
-    return Codes(*codes)
+    return Codes._make(_fast_call(
+        _fast.swiglu_backward, "fp8bw_swiglu_backward_quantize", gu, stream,
+        da, gu, pow2))
 
 
 def newton_schulz_batch(gs, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
