@@ -13,9 +13,11 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 namespace {
 
@@ -28,12 +30,26 @@ using Swiglu = int (*)(const void*, int64_t, int64_t, void*, float*, void*, floa
 using SwigluBwd = int (*)(const void*, const void*, int64_t, int64_t, void*, float*, void*, float*,
                           void*);
 
+struct NsJob {       // fp8bw_ns_job
+  const void* g;
+  int64_t n, k;
+  void* out;
+};
+using NewtonSchulzWs = int64_t (*)(const NsJob*, int);
+using NewtonSchulz = int (*)(const NsJob*, int, int, int, float, float, float, float, void*,
+                             int64_t, void*);
+
+constexpr int kFunctions = 10;
+constexpr Py_ssize_t kNsJobs = 8;      // matrices per call of the library
+
 struct Library {
   RmsNorm rmsnorm[2];          // by pow2
   RmsNormBwdWs rmsnorm_bwd_ws;
   RmsNormBwd rmsnorm_bwd;
   Swiglu swiglu[2];
   SwigluBwd swiglu_bwd[2];
+  NewtonSchulzWs ns_ws;
+  NewtonSchulz ns;
 } lib;
 
 // A refused argument (ValueError in Python).
@@ -266,11 +282,68 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (list of matrices, steps, a, b, c, eps) -> one bf16 result per matrix; up to
+// kNsJobs per call of the library, with one workspace for all of them.
+PyObject* newton_schulz(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 6)) return nullptr;
+  if (!PyList_Check(a[0])) {
+    PyErr_SetString(PyExc_TypeError, "expected a list of tensors");
+    return nullptr;
+  }
+  const long steps = PyLong_AsLong(a[1]);
+  double c[4];
+  for (int i = 0; i < 4; ++i) c[i] = PyFloat_AsDouble(a[2 + i]);
+  if (PyErr_Occurred()) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Py_ssize_t count = PyList_GET_SIZE(a[0]);
+    std::vector<NsJob> jobs(static_cast<size_t>(count));
+    std::vector<at::Tensor> outs(static_cast<size_t>(count));
+    if (count == 0) return result(0, {});
+    const at::Tensor& first = tensor(PyList_GET_ITEM(a[0], 0), "gs[0]");
+    const at::ScalarType type = first.scalar_type();
+    const at::Device dev = first.device();
+    if (type != at::kBFloat16 && type != at::kFloat)
+      throw Refused(std::string("gs: expected bf16 or fp32 tensors, got ") + at::toString(type));
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const std::string name = "gs[" + std::to_string(i) + "]";
+      const at::Tensor& g = tensor(PyList_GET_ITEM(a[0], i), name.c_str());
+      if (g.scalar_type() != type || g.dim() != 2)
+        throw Refused(name + ": expected a 2-D " + at::toString(type) + " tensor, got " +
+                      at::toString(g.scalar_type()) + " " + shape_text(g.sizes()));
+      jobs[i] = NsJob{input(g, type, g.sizes(), name.c_str(), dev), g.size(0), g.size(1), nullptr};
+    }
+    need_cuda(dev);
+    int64_t size = 0;
+    for (Py_ssize_t i = 0; i < count; i += kNsJobs) {
+      const int64_t need = lib.ns_ws(&jobs[i], static_cast<int>(std::min(kNsJobs, count - i)));
+      if (need < 0) return result(static_cast<int>(need), {});
+      size = std::max(size, need);
+    }
+    const c10::cuda::CUDAGuard guard(dev);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      outs[i] = empty({jobs[i].n, jobs[i].k}, at::kBFloat16, dev);
+      jobs[i].out = outs[i].data_ptr();
+    }
+    const at::Tensor ws = empty({size}, at::kByte, dev);
+    int st = 0;
+    for (Py_ssize_t i = 0; i < count && st == 0; i += kNsJobs)
+      st = lib.ns(&jobs[i], static_cast<int>(std::min(kNsJobs, count - i)), type == at::kFloat,
+                  static_cast<int>(steps), static_cast<float>(c[0]), static_cast<float>(c[1]),
+                  static_cast<float>(c[2]), static_cast<float>(c[3]), ptr(ws), size,
+                  stream_of(dev));
+    PyObject* r = PyTuple_New(count + 1);
+    if (r == nullptr) return nullptr;
+    PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
+    for (Py_ssize_t i = 0; i < count; ++i) PyTuple_SET_ITEM(r, i + 1, THPVariable_Wrap(outs[i]));
+    return r;
+  });
+}
+
 // Addresses of the library's functions, in the order of Library.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 8)) return nullptr;
-  void* p[8];
-  for (int i = 0; i < 8; ++i) {
+  if (!count_is(n, kFunctions)) return nullptr;
+  void* p[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -285,6 +358,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   lib.swiglu[1] = reinterpret_cast<Swiglu>(p[5]);
   lib.swiglu_bwd[0] = reinterpret_cast<SwigluBwd>(p[6]);
   lib.swiglu_bwd[1] = reinterpret_cast<SwigluBwd>(p[7]);
+  lib.ns_ws = reinterpret_cast<NewtonSchulzWs>(p[8]);
+  lib.ns = reinterpret_cast<NewtonSchulz>(p[9]);
   Py_RETURN_NONE;
 }
 
@@ -295,6 +370,7 @@ PyMethodDef methods[] = {
     {"rmsnorm_backward", FAST(rmsnorm_backward), METH_FASTCALL, nullptr},
     {"swiglu", FAST(swiglu), METH_FASTCALL, nullptr},
     {"swiglu_backward", FAST(swiglu_backward), METH_FASTCALL, nullptr},
+    {"newton_schulz", FAST(newton_schulz), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -34,7 +34,8 @@ def _bind(lib):
         "fp8bw_rmsnorm_quantize", "fp8bw_rmsnorm_quantize_pow2",
         "fp8bw_rmsnorm_backward_workspace", "fp8bw_rmsnorm_backward",
         "fp8bw_swiglu_quantize", "fp8bw_swiglu_quantize_pow2",
-        "fp8bw_swiglu_backward_quantize", "fp8bw_swiglu_backward_quantize_pow2")))
+        "fp8bw_swiglu_backward_quantize", "fp8bw_swiglu_backward_quantize_pow2",
+        "fp8bw_newton_schulz_workspace", "fp8bw_newton_schulz")))
 
 
 _bind(_lib)
@@ -387,7 +388,6 @@ def fp8bw_check_device_error(stream=None, device=None):
 # (include/fp8bw_layer.h)
 
 _NS_COEFFS = (3.4445, -4.7750, 2.0315)
-_NS_MAX_JOBS = 8
 
 
 def _pad16(rows):
@@ -637,17 +637,9 @@ def newton_schulz_batch(gs, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
     gs = list(gs)
     if not gs:
         return []
-    parts = [gs[i:i + _NS_MAX_JOBS] for i in range(0, len(gs), _NS_MAX_JOBS)]
-    dev = _device_of(gs)
-    with _allocating(stream, dev):
-        outs = [torch.empty(tuple(g.shape), dtype=torch.bfloat16, device=dev)
-                for g in gs]
-        ws = torch.empty((max(newton_schulz_workspace(p) for p in parts),),
-                         dtype=torch.uint8, device=dev)
-    for i, part in enumerate(parts):
-        fp8bw_newton_schulz(part, outs[i * _NS_MAX_JOBS:(i + 1) * _NS_MAX_JOBS],
-                            ws, steps, coeffs, eps, stream)
-    return outs
+    a, b, c = coeffs
+    return list(_fast_call(_fast.newton_schulz, "fp8bw_newton_schulz", gs[0],
+                           stream, gs, steps, a, b, c, eps))
 
 
 def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
