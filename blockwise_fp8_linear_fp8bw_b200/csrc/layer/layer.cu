@@ -110,23 +110,29 @@ int launched(cudaError_t e) {
 }
 
 // ---------------------------------------------------------------- tensor maps
+int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (encode == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || p == nullptr)
+      return FP8BW_ERR_CUDA;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  *out = encode;
+  return FP8BW_OK;
+}
+
 int encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
               uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
               CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (encode == nullptr) {
-      void* p = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
-              cudaSuccess ||
-          q != cudaDriverEntryPointSuccess || p == nullptr)
-        return FP8BW_ERR_CUDA;
-      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-  }
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  const int st = tensor_map_encoder(&encode);
+  if (st != FP8BW_OK) return st;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
@@ -424,31 +430,33 @@ constexpr int kMaxSteps = 64;
 constexpr int64_t kMaxNsDim = int64_t(1) << 17;
 
 struct NsBuffers {
-  uint16_t* hi[2];
+  uint16_t* hi[2];       // the iterate, alternating
   uint16_t* lo;
-  uint16_t* a;
-  uint16_t* b;
+  uint16_t* m[3];        // matrices of the short side
   double* part;
 };
 
 int64_t ns_align(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+// Elements per row of a workspace matrix.
+int64_t ns_pitch(int64_t cols) { return cdiv(cols, 64) * 64; }
+
 int64_t ns_job_bytes(int64_t n, int64_t k) {
   if (n == 0 || k == 0) return 0;
   const int64_t r = std::min(n, k);
-  return 3 * ns_align(2 * n * k) + 2 * ns_align(2 * r * r) + ns_align(8 * ns::kNormBlocks);
+  return 3 * ns_align(2 * n * ns_pitch(k)) + 3 * ns_align(2 * r * ns_pitch(r)) +
+         ns_align(8 * ns::kNormBlocks);
 }
 
 NsBuffers ns_carve(uint8_t* p, int64_t n, int64_t k) {
   const int64_t r = std::min(n, k);
-  const int64_t x = ns_align(2 * n * k), m = ns_align(2 * r * r);
+  const int64_t x = ns_align(2 * n * ns_pitch(k)), m = ns_align(2 * r * ns_pitch(r));
   NsBuffers b;
   b.hi[0] = reinterpret_cast<uint16_t*>(p);
   b.hi[1] = reinterpret_cast<uint16_t*>(p + x);
   b.lo = reinterpret_cast<uint16_t*>(p + 2 * x);
-  b.a = reinterpret_cast<uint16_t*>(p + 3 * x);
-  b.b = reinterpret_cast<uint16_t*>(p + 3 * x + m);
-  b.part = reinterpret_cast<double*>(p + 3 * x + 2 * m);
+  for (int i = 0; i < 3; ++i) b.m[i] = reinterpret_cast<uint16_t*>(p + 3 * x + i * m);
+  b.part = reinterpret_cast<double*>(p + 3 * x + 3 * m);
   return b;
 }
 
@@ -456,41 +464,43 @@ bool ns_dims_ok(int64_t n, int64_t k) {
   return n >= 0 && k >= 0 && n % 16 == 0 && k % 16 == 0 && n <= kMaxNsDim && k <= kMaxNsDim;
 }
 
-// One GEMM over all jobs: an operand is a 16-bit matrix with `rows` rows of
-// `cols` contiguous elements, read K-major (contraction along the row) or
-// MN-major.
+// One GEMM over all jobs: an operand is a workspace matrix with `rows` rows of
+// `pitch` elements, read K-major (contraction along the row) or MN-major.
 struct NsOperand {
   const uint16_t* p;
-  int64_t rows, cols;
+  int64_t rows, pitch;
   bool mn;
 };
 struct NsGemm {
   NsOperand a, b;
-  const uint16_t* c;      // poly: A; update, last: the old hi
-  const uint16_t* lo;
+  const uint16_t* c;
+  const uint16_t* c2;
   uint16_t* out;
+  uint16_t* lo;           // not null: the result is an iterate, split into out and lo
   int64_t rows, cols, kc;
+  int64_t pitch;          // of c and c2, and of out unless it is the caller's
+  bool sym, bf16;
+  float alpha, beta, beta2, diag;
 };
 
-int64_t ns_tiles(const NsGemm& g, int bn, bool sym) {
+int64_t ns_tiles(const NsGemm& g, int bn) {
   const int64_t tm = cdiv(g.rows, 256), tn = cdiv(g.cols, bn);
-  if (!sym) return tm * tn;
+  if (!g.sym) return tm * tn;
   const int64_t per = 256 / bn;
   return tm * tn - per * (tm * (tm - 1) / 2);
 }
 
 // The longest cluster's time under the kernel's tile order, in chunks of a
-// 256-wide tile. Operands reach the SMs at 8.7 TB/s at most (measured, whatever
-// the tile width, ring depth or tile order), which is what a chunk costs:
-// 32 KB per CTA with 256 columns, 24 KB with 128. A tile also costs about two
-// chunks of pipeline fill.
-double ns_makespan(const NsGemm* g, int count, int bn, bool sym, int clusters) {
-  const double chunk = bn == 256 ? 1.0 : 0.75;
+// 256-wide tile. A chunk costs what its two operand boxes cost the TMA unit (120
+// cycles each, and 64 bytes a cycle): 1260 cycles with 256 columns (32 + 32 KB),
+// 1010 with 128 (32 + 16 KB). A tile also costs about a chunk of pipeline fill.
+double ns_makespan(const NsGemm* g, int count, int bn, int clusters) {
+  const double chunk = bn == 256 ? 1.0 : 0.8;
   int64_t total = 0;
   double sum = 0.0;
   for (int i = 0; i < count; ++i) {
-    total += ns_tiles(g[i], bn, sym);
-    sum += static_cast<double>(ns_tiles(g[i], bn, sym)) * (cdiv(g[i].kc, ns::BK) + 2) * chunk;
+    total += ns_tiles(g[i], bn);
+    sum += static_cast<double>(ns_tiles(g[i], bn)) * (cdiv(g[i].kc, ns::BK) + 1) * chunk;
   }
   const int64_t waves = cdiv(total, clusters);
   if (waves > 16) return sum / clusters;      // the last wave hardly counts
@@ -501,19 +511,32 @@ double ns_makespan(const NsGemm* g, int count, int bn, bool sym, int clusters) {
       int64_t t = k * clusters + ((k & 1) ? clusters - 1 - c : c);
       if (t >= total) continue;
       int i = 0;
-      while (t >= ns_tiles(g[i], bn, sym)) t -= ns_tiles(g[i++], bn, sym);
-      w += static_cast<double>(cdiv(g[i].kc, ns::BK) + 2) * chunk;
+      while (t >= ns_tiles(g[i], bn)) t -= ns_tiles(g[i++], bn);
+      w += static_cast<double>(cdiv(g[i].kc, ns::BK) + 1) * chunk;
     }
     worst = std::max(worst, w);
   }
   return worst;
 }
 
+// 3-D view [column block of 64][row][64] of a workspace matrix; boxes of two
+// blocks x `rows` rows (K-major), or of `blocks` blocks x BK rows (MN-major).
 int encode_operand(CUtensorMap* map, const NsOperand& o, int rows) {
-  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, o.p, static_cast<uint64_t>(o.cols),
-                   static_cast<uint64_t>(o.rows), static_cast<uint64_t>(2 * o.cols), 64,
-                   o.mn ? 64 : rows, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  const int st = tensor_map_encoder(&encode);
+  if (st != FP8BW_OK) return st;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(o.rows),
+                              static_cast<cuuint64_t>(o.pitch / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * o.pitch), 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(o.mn ? ns::BK : rows),
+                             static_cast<cuuint32_t>(o.mn ? rows / 64 : 2)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(o.p), dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FP8BW_OK
+             : FP8BW_ERR_CUDA;
 }
 
 int encode_boxes(CUtensorMap* map, const void* p, int64_t rows, int64_t cols) {
@@ -522,18 +545,10 @@ int encode_boxes(CUtensorMap* map, const void* p, int64_t rows, int64_t cols) {
                    CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-// Everything a launch of one phase needs, prepared once per call.
-struct NsLaunch {
-  ns::Maps maps;
-  ns::Args args;
-  int bn = 256;
-  int clusters = 0;
-};
-
-template <int BN, int MODE>
+template <int BN>
 int ns_clusters(const Device& dev, int* clusters) {
   static DevicePrep prep;
-  auto kernel = ns::ns_gemm_kernel<BN, MODE>;
+  auto kernel = ns::ns_gemm_kernel<BN>;
   return prepare_for_device(prep, dev.ordinal, clusters, [&](int* out) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ns::Layout<BN>::kAlloc) != cudaSuccess)
@@ -555,59 +570,141 @@ int ns_clusters(const Device& dev, int* clusters) {
   });
 }
 
-template <int MODE>
-int ns_prepare(NsLaunch* l, const NsGemm* in, int count, const Device& dev) {
-  constexpr bool kSym = MODE == ns::kGram || MODE == ns::kPoly;
-  NsGemm g[ns::kMaxJobs];
-  std::copy(in, in + count, g);
+// One launch over the products g[0 .. count).
+int ns_launch(NsGemm* g, int count, const Device& dev, cudaStream_t stream) {
   // long contractions first (see the kernel's tile order)
   std::stable_sort(g, g + count, [](const NsGemm& x, const NsGemm& y) { return x.kc > y.kc; });
   int c256 = 0, c128 = 0;
-  int st = ns_clusters<256, MODE>(dev, &c256);
-  if (st == FP8BW_OK) st = ns_clusters<128, MODE>(dev, &c128);
+  int st = ns_clusters<256>(dev, &c256);
+  if (st == FP8BW_OK) st = ns_clusters<128>(dev, &c128);
   if (st != FP8BW_OK) return st;
   // 128-wide tiles where they spread the work better over the clusters
-  l->bn = ns_makespan(g, count, 128, kSym, c128) < 0.97 * ns_makespan(g, count, 256, kSym, c256)
-              ? 128
-              : 256;
-  l->clusters = l->bn == 256 ? c256 : c128;
-  std::memset(&l->args, 0, sizeof l->args);
-  std::memset(&l->maps, 0, sizeof l->maps);
+  const int bn =
+      ns_makespan(g, count, 128, c128) < 0.97 * ns_makespan(g, count, 256, c256) ? 128 : 256;
+  ns::Maps maps;
+  ns::Args args;
+  std::memset(&maps, 0, sizeof maps);
+  std::memset(&args, 0, sizeof args);
   int64_t tiles = 0;
   for (int i = 0; i < count; ++i) {
-    ns::Job& j = l->args.job[i];
+    ns::Job& j = args.job[i];
     j.rows = static_cast<int>(g[i].rows);
     j.cols = static_cast<int>(g[i].cols);
-    j.tiles_m = static_cast<int>(cdiv(g[i].rows, 256));
-    j.tiles_n = static_cast<int>(cdiv(g[i].cols, l->bn));
+    j.tiles_n = static_cast<int>(cdiv(g[i].cols, bn));
     j.chunks = static_cast<int>(cdiv(g[i].kc, ns::BK));
-    j.a_mn = g[i].a.mn;
-    j.b_mn = g[i].b.mn;
-    tiles += ns_tiles(g[i], l->bn, kSym);
+    tiles += ns_tiles(g[i], bn);
     if (tiles > INT32_MAX / 2) return FP8BW_ERR_SHAPE;
     j.tile_end = static_cast<int>(tiles);
-    st = encode_operand(&l->maps.a[i], g[i].a, ns::BM);
-    if (st == FP8BW_OK) st = encode_operand(&l->maps.b[i], g[i].b, l->bn / 2);
-    if (st == FP8BW_OK && MODE != ns::kGram)
-      st = encode_boxes(&l->maps.c[i], g[i].c, g[i].rows, g[i].cols);
-    if (st == FP8BW_OK && !kSym) st = encode_boxes(&l->maps.lo[i], g[i].lo, g[i].rows, g[i].cols);
-    if (st == FP8BW_OK) st = encode_boxes(&l->maps.out[i], g[i].out, g[i].rows, g[i].cols);
+    j.pitch = static_cast<int>(g[i].pitch);
+    j.a_mn = g[i].a.mn;
+    j.b_mn = g[i].b.mn;
+    j.sym = g[i].sym;
+    j.split = g[i].lo != nullptr;
+    j.bf16 = g[i].bf16;
+    j.c = g[i].c;
+    j.c2 = g[i].c2;
+    j.alpha = g[i].alpha;
+    j.beta = g[i].beta;
+    j.beta2 = g[i].beta2;
+    j.diag = g[i].diag;
+    st = encode_operand(&maps.a[i], g[i].a, ns::BM);
+    if (st == FP8BW_OK) st = encode_operand(&maps.b[i], g[i].b, bn / 2);
+    if (st == FP8BW_OK && g[i].lo != nullptr)
+      st = encode_boxes(&maps.lo[i], g[i].lo, g[i].rows, g[i].cols);
+    if (st == FP8BW_OK) st = encode_boxes(&maps.out[i], g[i].out, g[i].rows, g[i].cols);
     if (st != FP8BW_OK) return st;
   }
-  l->args.count = count;
-  l->clusters = static_cast<int>(std::min<int64_t>(l->clusters, tiles));
-  return FP8BW_OK;
+  args.count = count;
+  const int clusters = static_cast<int>(std::min<int64_t>(bn == 256 ? c256 : c128, tiles));
+  const dim3 grid(2 * clusters), block(ns::kThreads);
+  if (bn == 256)
+    return launched(launch_kernel(ns::ns_gemm_kernel<256>, grid, block, ns::Layout<256>::kAlloc,
+                                  stream, maps, args));
+  return launched(launch_kernel(ns::ns_gemm_kernel<128>, grid, block, ns::Layout<128>::kAlloc,
+                                stream, maps, args));
 }
 
-template <int MODE>
-int ns_launch(const NsLaunch& l, cudaStream_t stream) {
-  const dim3 grid(2 * l.clusters), block(ns::kThreads);
-  if (l.bn == 256)
-    return launched(launch_kernel(ns::ns_gemm_kernel<256, MODE>, grid, block,
-                                  ns::Layout<256>::kAlloc, stream, l.maps, l.args));
-  return launched(launch_kernel(ns::ns_gemm_kernel<128, MODE>, grid, block,
-                                ns::Layout<128>::kAlloc, stream, l.maps, l.args));
-}
+// The products of one matrix's iteration.
+struct NsMatrix {
+  int64_t n, k, r, c, kp, rp;
+  bool tall, pairs;
+  NsBuffers w;
+  uint16_t* out;
+  int parity = 0;
+  float ca, cb, cc;
+
+  NsMatrix() = default;
+  NsMatrix(const fp8bw_ns_job& j, uint8_t* ws, float a, float b, float c_)
+      : n(j.n), k(j.k), r(std::min(j.n, j.k)), c(std::max(j.n, j.k)), kp(ns_pitch(j.k)),
+        rp(ns_pitch(std::min(j.n, j.k))), tall(j.n > j.k), w(ns_carve(ws, j.n, j.k)),
+        out(j.out), ca(a), cb(b), cc(c_) {
+    // A pair of steps trades 3 r^2 R flops for 3 r^3 and one launch: for R >= 3/2 r
+    // where the products are long beside a launch (2 r^2 R flops of 4 G: 4 us).
+    // P_1 P_0 - d_1 d_0 I has to stay below 64, its range at kQScale.
+    pairs = 2 * c >= 3 * r && static_cast<double>(r) * r * c >= 2e9 && std::fabs(ca) <= 5.0f &&
+            std::fabs(ca + cb + cc) <= 5.0f;
+  }
+
+  // d of P - d I at a step
+  float shift(int step) const { return step >= ns::kShiftStep ? ca + cb + cc : ca; }
+  NsOperand small(int i) const { return {w.m[i], r, rp, false}; }
+
+  // m[0] = X X^T
+  NsGemm gram() const {
+    NsGemm g{};
+    g.a = g.b = {w.hi[parity], n, kp, tall};
+    g.out = w.m[0];
+    g.rows = r;
+    g.cols = rp;
+    g.kc = c;
+    g.sym = true;
+    g.alpha = ns::kAScale / (ns::kXScale * ns::kXScale);
+    return g;
+  }
+  // m[o] = alpha m[x] m[y] + beta m[p] (symmetric; operands that commute)
+  NsGemm product(int o, int x, int y, int p, float alpha, float beta) const {
+    NsGemm g{};
+    g.a = small(x);
+    g.b = small(y);
+    g.c = w.m[p];
+    g.out = w.m[o];
+    g.rows = r;
+    g.cols = g.pitch = rp;
+    g.kc = r;
+    g.sym = true;
+    g.alpha = alpha;
+    g.beta = beta;
+    return g;
+  }
+  // m[o] = P - d I of A = m[x]
+  NsGemm poly(int o, int x, int step) const {
+    NsGemm g = product(o, x, x, x, cc / ns::kAScale, cb);
+    g.diag = (shift(step) - ca) * ns::kAScale;
+    return g;
+  }
+  // X <- d X + m[q] X / scale, or the result if `last`
+  NsGemm update(int q, float d, float scale, bool last) {
+    NsGemm g{};
+    const NsOperand x{w.hi[parity], n, kp, !tall};
+    g.a = tall ? x : small(q);
+    g.b = tall ? small(q) : x;
+    g.c = w.hi[parity];
+    g.c2 = w.lo;
+    g.rows = n;
+    g.kc = r;
+    g.pitch = kp;
+    const float out_scale = last ? 1.0f / ns::kXScale : 1.0f;
+    g.alpha = out_scale / scale;
+    g.beta = d * out_scale;
+    g.beta2 = g.beta / ns::kLoScale;
+    g.bf16 = last;
+    g.out = last ? out : w.hi[1 - parity];
+    g.lo = last ? nullptr : w.lo;
+    g.cols = last ? k : kp;
+    parity = 1 - parity;
+    return g;
+  }
+};
 
 int newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, float ca, float cb,
                   float cc, float eps, void* ws, int64_t ws_bytes, void* stream) {
@@ -634,88 +731,87 @@ int newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, 
   if (st != FP8BW_OK) return st;
 
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  fp8bw_ns_job live[ns::kMaxJobs];
-  NsBuffers buf[ns::kMaxJobs];
+  NsMatrix mat[ns::kMaxJobs];
   ns::InArgs in{};
   in.g_f32 = g_is_f32 != 0;
   in.eps = eps;
   int nl = 0;
   int64_t most = 0;
+  bool any_pairs = false;
   uint8_t* p = static_cast<uint8_t*>(ws);
   for (int i = 0; i < count; ++i) {
     const fp8bw_ns_job& j = jobs[i];
     if (j.n == 0 || j.k == 0) continue;
-    live[nl] = j;
-    buf[nl] = ns_carve(p, j.n, j.k);
+    mat[nl] = NsMatrix(j, p, ca, cb, cc);
     p += ns_job_bytes(j.n, j.k);
-    in.job[nl] = ns::InJob{j.g, j.n * j.k, buf[nl].part, buf[nl].hi[0], buf[nl].lo};
-    most = std::max(most, j.n * j.k);
+    const NsMatrix& m = mat[nl];
+    in.job[nl] = ns::InJob{j.g, j.n * j.k, static_cast<int>(j.k), static_cast<int>(m.kp),
+                           m.w.part, m.w.hi[0], m.w.lo};
+    most = std::max(most, j.n * m.kp);
+    any_pairs = any_pairs || m.pairs;
     ++nl;
   }
   if (nl == 0) return FP8BW_OK;
-
-  // the phases' launches: the iterate alternates between hi[0] and hi[1]
-  NsLaunch gram[2], poly, update[2], last;
-  for (int parity = 0; parity < 2; ++parity) {
-    NsGemm gg[ns::kMaxJobs], gu[ns::kMaxJobs], gl[ns::kMaxJobs];
-    for (int i = 0; i < nl; ++i) {
-      const int64_t n = live[i].n, k = live[i].k, r = std::min(n, k), c = std::max(n, k);
-      const bool tall = n > k;
-      const NsBuffers& w = buf[i];
-      const uint16_t* x = w.hi[parity];
-      gg[i] = NsGemm{{x, n, k, tall}, {x, n, k, tall}, nullptr, nullptr, w.a, r, r, c};
-      const NsOperand m{w.b, r, r, false};
-      if (tall)
-        gu[i] = NsGemm{{x, n, k, false}, m, x, w.lo, w.hi[1 - parity], n, k, r};
-      else
-        gu[i] = NsGemm{m, {x, n, k, true}, x, w.lo, w.hi[1 - parity], n, k, r};
-      gl[i] = gu[i];
-      gl[i].out = live[i].out;
-    }
-    if (parity < steps) {
-      st = ns_prepare<ns::kGram>(&gram[parity], gg, nl, dev);
-      if (st != FP8BW_OK) return st;
-      gram[parity].args.alpha = ns::kAScale / (ns::kXScale * ns::kXScale);
-    }
-    if (parity < steps - 1) {
-      st = ns_prepare<ns::kUpdate>(&update[parity], gu, nl, dev);
-      if (st != FP8BW_OK) return st;
-      update[parity].args.alpha = 1.0f / ns::kAScale;
-    }
-    if (parity == ((steps - 1) & 1)) {
-      st = ns_prepare<ns::kLast>(&last, gl, nl, dev);
-      if (st != FP8BW_OK) return st;
-      last.args.alpha = 1.0f / (ns::kAScale * ns::kXScale);
-    }
-  }
-  {
-    NsGemm gp[ns::kMaxJobs];
-    for (int i = 0; i < nl; ++i) {
-      const int64_t r = std::min(live[i].n, live[i].k);
-      const NsOperand m{buf[i].a, r, r, false};
-      gp[i] = NsGemm{m, m, buf[i].a, nullptr, buf[i].b, r, r, r};
-    }
-    st = ns_prepare<ns::kPoly>(&poly, gp, nl, dev);
-    if (st != FP8BW_OK) return st;
-    poly.args.alpha = cc / ns::kAScale;
-    poly.args.beta = cb;
-  }
 
   st = launched(launch_kernel(ns::ns_sumsq_kernel, dim3(ns::kNormBlocks, nl),
                               dim3(ns::kSplitThreads), 0, cs, in));
   if (st != FP8BW_OK) return st;
   const int64_t blocks = std::min<int64_t>(cdiv(most, 8 * ns::kSplitThreads), 8 * dev.sm_count / nl);
-  st = launched(launch_kernel(ns::ns_split_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, blocks)), nl),
+  st = launched(launch_kernel(ns::ns_split_kernel,
+                              dim3(static_cast<unsigned>(std::max<int64_t>(1, blocks)), nl),
                               dim3(ns::kSplitThreads), 0, cs, in));
-  for (int i = 0; st == FP8BW_OK && i < steps; ++i) {
-    const float shift = i >= ns::kShiftStep ? cb + cc : 0.0f;
-    poly.args.diag = shift * ns::kAScale;
-    update[i & 1].args.beta = ca + shift;
-    last.args.beta = (ca + shift) / ns::kXScale;
-    st = ns_launch<ns::kGram>(gram[i & 1], cs);
-    if (st == FP8BW_OK) st = ns_launch<ns::kPoly>(poly, cs);
-    if (st != FP8BW_OK) break;
-    st = i + 1 < steps ? ns_launch<ns::kUpdate>(update[i & 1], cs) : ns_launch<ns::kLast>(last, cs);
+
+  // One launch: what `make(matrix, &gemm)` gives for every matrix it returns
+  // true for.
+  auto launch = [&](auto&& make) {
+    if (st != FP8BW_OK) return;
+    NsGemm g[ns::kMaxJobs];
+    int n = 0;
+    for (int i = 0; i < nl; ++i)
+      if (make(mat[i], &g[n])) ++n;
+    if (n > 0) st = ns_launch(g, n, dev, cs);
+  };
+  const float a = ns::kAScale;
+  for (int i = 0; st == FP8BW_OK && i < steps;) {
+    // the first two steps and, from five steps on, the last two as a pair
+    const bool pair = any_pairs && i + 2 <= steps &&
+                      (i == 0 || (steps >= 5 && i == steps - 2));
+    const bool last = i + (pair ? 2 : 1) == steps;
+    launch([&](NsMatrix& m, NsGemm* g) { return *g = m.gram(), true; });
+    launch([&](NsMatrix& m, NsGemm* g) { return *g = m.poly(1, 0, i), true; });
+    if (pair) {
+      // matrices that take no pairs go on step by step in the same launches
+      launch([&](NsMatrix& m, NsGemm* g) {
+        *g = m.pairs ? m.product(2, 1, 0, 0, 1.0f / a, m.shift(i))          // T = P_0 A_0
+                     : m.update(1, m.shift(i), a, false);
+        return true;
+      });
+      launch([&](NsMatrix& m, NsGemm* g) {
+        *g = m.pairs ? m.product(0, 2, 1, 2, 1.0f / a, m.shift(i)) : m.gram();   // A_1 = T P_0
+        return true;
+      });
+      launch([&](NsMatrix& m, NsGemm* g) {
+        return *g = m.pairs ? m.poly(2, 0, i + 1) : m.poly(1, 0, i + 1), true;
+      });
+      launch([&](NsMatrix& m, NsGemm* g) {
+        if (!m.pairs) return false;
+        // P_1 P_0 - d_1 d_0 I
+        *g = m.product(0, 1, 2, 1, ns::kQScale / (a * a), m.shift(i + 1) * ns::kQScale / a);
+        g->c2 = m.w.m[2];
+        g->beta2 = m.shift(i) * ns::kQScale / a;
+        return true;
+      });
+      launch([&](NsMatrix& m, NsGemm* g) {
+        *g = m.pairs ? m.update(0, m.shift(i) * m.shift(i + 1), ns::kQScale, last)
+                     : m.update(1, m.shift(i + 1), a, last);
+        return true;
+      });
+    } else {
+      launch([&](NsMatrix& m, NsGemm* g) {
+        return *g = m.update(1, m.shift(i), a, last), true;
+      });
+    }
+    i += pair ? 2 : 1;
   }
   return st;
 }

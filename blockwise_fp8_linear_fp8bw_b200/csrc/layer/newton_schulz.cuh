@@ -2,14 +2,26 @@
 // products on the tensor cores (sm_100a, tcgen05 on CTA pairs).
 //
 //   X_0 = G / (||G||_F + eps)
-//   A = X X^T,  B = b A + c A A,  X <- a X + B X          (rows <= columns)
-//   A = X^T X,  B = b A + c A A,  X <- a X + X B          (rows >  columns)
-// so A and B are r x r with r the shorter side. A step is three launches of
-// one GEMM kernel, each over all jobs (matrices) of the call:
-//   gram    A, only its tiles on and above the diagonal; each of the others is
-//           written as the transpose of its mirror image from the same registers
-//   poly    B, likewise (A is symmetric, so A A = A A^T)
-//   update  the new X, added to a X in the epilogue
+//   A = X X^T,  P = a I + b A + c A A,  X <- P X          (rows <= columns)
+//   A = X^T X,  P = a I + b A + c A A,  X <- X P          (rows >  columns)
+// so A and P are r x r with r the shorter side (R the longer one). Every product
+// is a launch of one GEMM kernel over all jobs (matrices) of the call; products
+// of A, P and the like are symmetric: only tiles on and above the diagonal are
+// computed, the others written as their mirror images from the same registers.
+//
+// A step on its own is three products (r^2 R, r^3 and 2 r^2 R flops). Two steps
+// in a row can be taken on the short side alone, for A, P and their products
+// commute:
+//   A_1 = P_0 A_0 P_0,   X_2 = (P_1 P_0) X_0
+// which saves the first of the two updates and the second Gram product (3 r^2 R)
+// for three products more (T = P_0 A_0, A_1 = T P_0, P_1 P_0; r^3 each). That pays
+// for oblong matrices. What is lost is that A_1 is no longer made from an X that
+// exists: its rounding errors are amplified by up to a^2 = 12 for small singular
+// values. That is harmless in the first pair (A is small) and in the last (no
+// singular value is), so only those are taken so: for five steps 2 + 1 + 2.
+// (Simulated against 64 bits, 256 x 1536, errors of the bf16 result: Gaussian
+// matrix 1.9e-3 step by step, 2.0e-3 with pairs; some directions 300 times the
+// rest 1.8e-3 and 2.3e-3; all steps in one pair-like run: not finite.)
 //
 // Numbers. Operands are fp16 (11 significant bits; bf16's 8 lose 1% of the
 // result in five steps), products accumulate in fp32. The iterate itself is
@@ -30,62 +42,79 @@ namespace ns {
 
 constexpr int kMaxJobs = 8;
 constexpr int BM = 128;            // rows per CTA; a pair computes 256
-constexpr int BK = 64;             // contraction chunk: 128 bytes of fp16
+constexpr int BK = 128;            // contraction chunk: two blocks of 64 (128 bytes)
 constexpr int kThreads = 384;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kNumEpiWarps = 8;
 constexpr float kXScale = 1024.0f;     // X is stored times this
-constexpr float kAScale = 4096.0f;     // A and B are stored times this
+constexpr float kAScale = 4096.0f;     // A, P - d I and T are stored times this
+constexpr float kQScale = 1024.0f;     // P_1 P_0 - d_1 d_0 I is stored times this
 constexpr float kLoScale = 2048.0f;    // lo = (x - hi) * this
 
 constexpr int kShiftStep = 3;
 
-enum Mode : int { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3 };
-
+// result = alpha * product + beta * C + beta2 * C2, minus diag on the diagonal
 struct Job {
-  int rows, cols;            // output
-  int tiles_m, tiles_n;      // 256 x BN tiles
+  int rows, cols;            // output; cols as stored, including padding columns
+  int tiles_n;               // tiles of BN columns per row of tiles
   int chunks;                // of the contraction
-  int a_mn, b_mn;            // operand stored with the contraction outermost
   int tile_end;              // cumulative tile count
+  int pitch;                 // elements per row of C and C2
+  uint8_t a_mn, b_mn;        // operand stored with the contraction outermost
+  uint8_t sym;               // symmetric result: see above
+  uint8_t split;             // the result is an iterate: hi to out, lo to lo
+  uint8_t bf16;              // the result is bf16, not fp16
+  const uint16_t* c;         // may be null
+  const uint16_t* c2;        // may be null
+  float alpha, beta, beta2, diag;
 };
 
+// Matrices in the workspace have rows of a multiple of 64 elements, the padding
+// columns zero, so that a 3-D view [column block][row][64] is exact and one copy
+// can bring two blocks: an operand's share of a chunk is one 32 KB box. (The TMA
+// unit spends about 120 cycles on a box besides 64 bytes a cycle: boxes of 8, 16
+// and 32 KB reach 64, 84 and 101 GB/s per SM.)
 struct Maps {
   CUtensorMap a[kMaxJobs];     // operands
   CUtensorMap b[kMaxJobs];
-  CUtensorMap c[kMaxJobs];     // poly: A; update, last: the old hi  (32 x 32 boxes)
-  CUtensorMap lo[kMaxJobs];    // update, last: lo
-  CUtensorMap out[kMaxJobs];   // the result
+  CUtensorMap lo[kMaxJobs];    // split results: lo, written in place (32 x 32 boxes)
+  CUtensorMap out[kMaxJobs];   // the result (32 x 32 boxes)
 };
 
 struct Args {
   Job job[kMaxJobs];
   int count;
-  float alpha, beta;           // result = alpha * product + beta * C
-  float diag;                  // poly: minus this on the diagonal
 };
 
 template <int BN_>
 struct Layout {
   static constexpr int BN = BN_;
-  static constexpr int kStages = BN == 256 ? 4 : 5;
+  static constexpr int kStages = BN == 256 ? 3 : 4;
   static constexpr int kTmemBufs = 512 / BN;
   static constexpr int kABytes = BM * BK * 2;
   static constexpr int kBBytes = (BN / 2) * BK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kSlots = 3;                 // C / result boxes per warp
-  static constexpr int kAhead = kSlots - 1;        // C boxes requested ahead
   static constexpr int kBoxBytes = 32 * 32 * 2;
-  static constexpr int kSlotBytes = 2 * kBoxBytes;
+  static constexpr int kSlotBytes = 2 * kBoxBytes;   // staging of a result box, per warp
   static constexpr int kSlotOff = kRingBytes;
-  static constexpr int kBarOff = kSlotOff + kNumEpiWarps * kSlots * kSlotBytes;
-  static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 1 + kNumEpiWarps * kSlots;
+  static constexpr int kBarOff = kSlotOff + kNumEpiWarps * kSlotBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kBytes = kMiscOff + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
+
+// A box of a 3-D tensor; as tma_load_2d_pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t bar,
+                                                 int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::"
+      "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 
 // kind::f16 instruction descriptor: fp32 accumulator, fp16 operands, majorness
 // of A (bit 15) and B (bit 16), N >> 3 at bit 17, M >> 4 at bit 24.
@@ -124,14 +153,28 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
-// Tile `lt` of a job -> (tm, tn). Symmetric results (SYM) number only the
-// tiles that reach the diagonal's 256-row block or lie right of it.
-template <int BN, bool SYM>
-__device__ __forceinline__ void tile_at(int lt, int tiles_n, int& tm, int& tn) {
-  if constexpr (SYM) {
+// v += k * (the 32 fp16 values of c).
+__device__ __forceinline__ void add_scaled(float (&v)[32], const uint4 (&c)[4], float k) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_f16(w[e]);
+      v[8 * u + 2 * e] = fmaf(k, f.x, v[8 * u + 2 * e]);
+      v[8 * u + 2 * e + 1] = fmaf(k, f.y, v[8 * u + 2 * e + 1]);
+    }
+  }
+}
+
+// Tile `lt` of a job -> (tm, tn). Symmetric results number only the tiles that
+// reach the diagonal's 256-row block or lie right of it.
+template <int BN>
+__device__ __forceinline__ void tile_at(const Job& job, int lt, int& tm, int& tn) {
+  if (job.sym) {
     constexpr int kPer = 256 / BN;
     tm = 0;
-    int left = tiles_n;
+    int left = job.tiles_n;
     while (lt >= left) {
       lt -= left;
       left -= kPer;
@@ -139,8 +182,8 @@ __device__ __forceinline__ void tile_at(int lt, int tiles_n, int& tm, int& tn) {
     }
     tn = tm * kPer + lt;
   } else {
-    tm = lt / tiles_n;
-    tn = lt - tm * tiles_n;
+    tm = lt / job.tiles_n;
+    tn = lt - tm * job.tiles_n;
   }
 }
 
@@ -150,15 +193,12 @@ __device__ __forceinline__ void tile_at(int lt, int tiles_n, int& tm, int& tn) {
 // and write the result box by box (32 x 32) through shared memory and TMA. The
 // product of a whole tile stays in TMEM (512 / BN tiles fit), so the epilogue
 // of one tile runs under the MMAs of the next.
-template <int BN, int MODE>
+template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ns_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args args) {
   using L = Layout<BN>;
   constexpr int kStages = L::kStages;
   constexpr int kBufs = L::kTmemBufs;
-  constexpr bool kSym = MODE == kGram || MODE == kPoly;
-  constexpr bool kHasC = MODE != kGram;
-  constexpr bool kHasLo = MODE == kUpdate || MODE == kLast;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -170,7 +210,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + kBufs + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 2 * kBufs);
-  auto slot_bar = [&](int w, int s) { return drain_bar + 8u * (1 + w * L::kSlots + s); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMiscOff);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
@@ -189,7 +228,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(b), 2 * kNumEpiWarps);
     }
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < kNumEpiWarps * L::kSlots; ++i) mbar_init(slot_bar(0, i), 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -197,8 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tmap(&maps.a[lane]);
     prefetch_tmap(&maps.b[lane]);
     prefetch_tmap(&maps.out[lane]);
-    if (kHasC) prefetch_tmap(&maps.c[lane]);
-    if (kHasLo) prefetch_tmap(&maps.lo[lane]);
+    if (args.job[lane].split) prefetch_tmap(&maps.lo[lane]);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
@@ -238,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lt >= num_tiles) continue;
         const int j = find_job(lt);
         int tm, tn;
-        tile_at<BN, kSym>(lt, args.job[j].tiles_n, tm, tn);
+        tile_at<BN>(args.job[j], lt, tm, tn);
         const int a_row = tm * (2 * BM) + static_cast<int>(rank) * BM;
         const int b_row = tn * BN + static_cast<int>(rank) * (BN / 2);
         const int chunks = args.job[j].chunks;
@@ -254,19 +291,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t b_dst = a_dst + L::kABytes;
           const uint32_t fbar = full_leader0 + 8u * s;
           if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * L::kStageBytes);
-          if (a_mn) {
-            tma_load_2d_pair(a_dst, &maps.a[j], fbar, a_row, c * BK);
-            tma_load_2d_pair(a_dst + 64 * BK * 2, &maps.a[j], fbar, a_row + 64, c * BK);
-          } else {
-            tma_load_2d_pair(a_dst, &maps.a[j], fbar, c * BK, a_row);
-          }
-          if (b_mn) {
-            tma_load_2d_pair(b_dst, &maps.b[j], fbar, b_row, c * BK);
-            if constexpr (BN == 256)
-              tma_load_2d_pair(b_dst + 64 * BK * 2, &maps.b[j], fbar, b_row + 64, c * BK);
-          } else {
-            tma_load_2d_pair(b_dst, &maps.b[j], fbar, c * BK, b_row);
-          }
+          // K-major: rows of the operand, two 64-element blocks of the
+          // contraction; MN-major: 128 rows of the contraction, the blocks
+          // that hold this CTA's operand rows
+          if (a_mn)
+            tma_load_3d_pair(a_dst, &maps.a[j], fbar, 0, c * BK, a_row / 64);
+          else
+            tma_load_3d_pair(a_dst, &maps.a[j], fbar, 0, a_row, 2 * c);
+          if (b_mn)
+            tma_load_3d_pair(b_dst, &maps.b[j], fbar, 0, c * BK, b_row / 64);
+          else
+            tma_load_3d_pair(b_dst, &maps.b[j], fbar, 0, b_row, 2 * c);
         }
       }
       if (!ok && leader) {
@@ -296,13 +331,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int chunks = args.job[j].chunks;
         const bool a_mn = args.job[j].a_mn != 0, b_mn = args.job[j].b_mn != 0;
         const uint32_t idesc = idesc_f16(2 * BM, BN, a_mn, b_mn);
-        // K = 16 per instruction: 32 bytes along a K-major row, or 16 rows
-        // of 128 bytes of an MN-major tile (64-element atoms 8 KB apart)
+        // K = 16 per instruction: 32 bytes along a K-major row (four to a
+        // block), or 16 rows of 128 bytes of an MN-major tile, whose
+        // 64-element blocks are 16 KB apart
         const uint64_t ad0 = a_mn ? desc_mnmajor_sw128(sbase, 64 * BK * 2) : desc_kmajor_sw128(sbase);
         const uint64_t bd0 = b_mn ? desc_mnmajor_sw128(sbase + L::kABytes, 64 * BK * 2)
                                   : desc_kmajor_sw128(sbase + L::kABytes);
         const uint64_t as = a_mn ? (16 * 128) >> 4 : 32 >> 4;
         const uint64_t bs = b_mn ? (16 * 128) >> 4 : 32 >> 4;
+        const uint64_t ah = (a_mn ? 4 * 16 * 128 : L::kABytes / 2) >> 4;   // to the second half
+        const uint64_t bh = (b_mn ? 4 * 16 * 128 : L::kBBytes / 2) >> 4;
         const int tb = tc % kBufs;
         const uint32_t tu = tc / kBufs;
         ++tc;
@@ -326,7 +364,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (elected) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, idesc, c > 0 || kk > 0 ? 1u : 0u);
+              mma_f16_pair(d_tmem, ad + (kk >> 2) * ah + (kk & 3) * as,
+                           bd + (kk >> 2) * bh + (kk & 3) * bs, idesc, c > 0 || kk > 0 ? 1u : 0u);
             mma_commit_pair(empty_bar(s), 0x3);
           }
           __syncwarp();
@@ -348,150 +387,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int ew = warp - kFirstEpiWarp;
     const int hh = ew >> 2;                 // column half of the tile
     constexpr int kBoxes = BN / 2 / 32;
-    const uint32_t slot0 = sbase + L::kSlotOff + ew * L::kSlots * L::kSlotBytes;
+    const uint32_t slot = sbase + L::kSlotOff + ew * L::kSlotBytes;
     const uint32_t tempty_leader0 = mapa_shared(tempty_bar(0), 0);
     uint32_t tc = 0;
-    uint32_t loads = 0, used = 0;           // C boxes requested / consumed
-    uint32_t stores = 0;                    // result boxes written (no C)
-    bool ok = true;
-    for (int k = 0; ok && k < waves; ++k) {
+    for (int k = 0; k < waves; ++k) {
       int lt = tile_of(k);
       if (lt >= num_tiles) continue;
       const int j = find_job(lt);
       int tm, tn;
-      tile_at<BN, kSym>(lt, args.job[j].tiles_n, tm, tn);
-      const int rows = args.job[j].rows, cols = args.job[j].cols;
+      tile_at<BN>(args.job[j], lt, tm, tn);
+      const Job& job = args.job[j];
+      const int rows = job.rows, cols = job.cols;
       const int y0 = tm * (2 * BM) + static_cast<int>(rank) * BM + q * 32;
       const int x0 = tn * BN + hh * (BN / 2);
-      const bool mirror = kSym && tn * BN >= (tm + 1) * (2 * BM);
+      const bool mirror = job.sym && tn * BN >= (tm + 1) * (2 * BM);
+      const bool split = job.split, bf16 = job.bf16;
+      const uint16_t* cp = job.c;
+      const uint16_t* cp2 = job.c2;
+      const float alpha = job.alpha, beta = job.beta, beta2 = job.beta2, diag = job.diag;
       // boxes of this warp that hold anything
       const int boxes = y0 < rows && x0 < cols ? min(kBoxes, (cols - x0 + 31) / 32) : 0;
-      // C of box gi into the next slot; before that, the stores that used the
-      // slot must have read it
+      // C of box gi: this lane's row, 32 columns, loaded a box ahead (the first
+      // one under the tile's products)
+      uint4 ch[4], cl[4];
+      const bool row_in = y0 + lane < rows;
+      const int64_t c_at = static_cast<int64_t>(y0 + lane) * job.pitch + x0;
       auto load_c = [&](int gi) {
-        const int s = loads % L::kSlots;
-        if (lane == 0) {
-          bulk_wait_group_read<L::kSlots - L::kAhead>();
-          const uint32_t dst = slot0 + s * L::kSlotBytes;
-          mbar_arrive_expect_tx(slot_bar(ew, s), kHasLo ? 2 * L::kBoxBytes : L::kBoxBytes);
-          tma_load_2d(dst, &maps.c[j], slot_bar(ew, s), x0 + gi * 32, y0);
-          if constexpr (kHasLo)
-            tma_load_2d(dst + L::kBoxBytes, &maps.lo[j], slot_bar(ew, s), x0 + gi * 32, y0);
+        if (cp != nullptr) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            ch[u] = row_in ? *reinterpret_cast<const uint4*>(cp + c_at + gi * 32 + u * 8)
+                           : make_uint4(0u, 0u, 0u, 0u);
         }
-        ++loads;
+        if (cp2 != nullptr) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            cl[u] = row_in ? *reinterpret_cast<const uint4*>(cp2 + c_at + gi * 32 + u * 8)
+                           : make_uint4(0u, 0u, 0u, 0u);
+        }
       };
-      if constexpr (kHasC) {
-        if (boxes > 0) {
-          if (lane == 0) bulk_wait_group_read<0>();
-          for (int gi = 0; gi < L::kAhead && gi < boxes; ++gi) load_c(gi);
-        }
-      }
+      if (boxes > 0) load_c(0);
       const int tb = tc % kBufs;
       const uint32_t tu = tc / kBufs;
       ++tc;
-      if (!mbar_wait(tfull_bar(tb), tu & 1u, abort_flag, kErrTimeoutEpi)) {
-        ok = false;
-        break;
-      }
+      if (!mbar_wait(tfull_bar(tb), tu & 1u, abort_flag, kErrTimeoutEpi)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(tb * BN + hh * (BN / 2));
       for (int gi = 0; gi < boxes; ++gi) {
         uint32_t r[32];
         tmem_ld32(taddr + gi * 32, r);
-        uint32_t slot;
-        if constexpr (kHasC) {
-          const int s = used % L::kSlots;
-          if (!mbar_wait(slot_bar(ew, s), (used / L::kSlots) & 1u, abort_flag, kErrTimeoutEpi)) {
-            ok = false;
-            break;
-          }
-          ++used;
-          slot = slot0 + s * L::kSlotBytes;
-        } else {
-          slot = slot0 + (stores % L::kSlots) * L::kSlotBytes;
-          ++stores;
-          if (lane == 0) bulk_wait_group_read<L::kSlots - 1>();
-          __syncwarp();
-        }
         tmem_wait_ld();
         tmem_regs_ready(r);
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * alpha;
+        if (cp2 != nullptr) add_scaled(v, cl, beta2);
+        if (cp != nullptr) add_scaled(v, ch, beta);
+        if (y0 == x0 + gi * 32) {      // a box on the diagonal
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] -= e == lane ? diag : 0.0f;
+        }
+        if (gi + 1 < boxes) load_c(gi + 1);
+        // the last box's stores must have read the staging buffer
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
 #pragma unroll
         for (int u = 0; u < 4; ++u) {        // 16-byte units of the row's 64 bytes
           const uint32_t at = slot + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4);
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * u + e]) * args.alpha;
-          if constexpr (kHasC) {
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(at)
-                         : "memory");
-            float c[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack_f16(w[e]);
-              c[2 * e] = f.x;
-              c[2 * e + 1] = f.y;
-            }
-            if constexpr (kHasLo) {
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(at + L::kBoxBytes)
-                           : "memory");
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_f16(w[e]);
-                c[2 * e] = fmaf(f.x, 1.0f / kLoScale, c[2 * e]);
-                c[2 * e + 1] = fmaf(f.y, 1.0f / kLoScale, c[2 * e + 1]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(args.beta, c[e], v[e]);
-            if constexpr (MODE == kPoly) {
-              if (y0 == x0 + gi * 32) {      // a box on the diagonal
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] -= 8 * u + e == lane ? args.diag : 0.0f;
-              }
-            }
-          }
+          const float* w = v + 8 * u;
           uint32_t o[4];
-          if constexpr (MODE == kLast) {
+          if (bf16) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(w[2 * e], w[2 * e + 1]);
               o[e] = *reinterpret_cast<uint32_t*>(&b2);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pack_f16(v[2 * e], v[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) o[e] = pack_f16(w[2 * e], w[2 * e + 1]);
           }
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]),
                        "r"(o[2]), "r"(o[3])
                        : "memory");
-          if constexpr (MODE == kUpdate) {
+          if (split) {
             uint32_t l[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 hv = unpack_f16(o[e]);
-              l[e] = pack_f16((v[2 * e] - hv.x) * kLoScale, (v[2 * e + 1] - hv.y) * kLoScale);
+              l[e] = pack_f16((w[2 * e] - hv.x) * kLoScale, (w[2 * e + 1] - hv.y) * kLoScale);
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + L::kBoxBytes),
                          "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3])
                          : "memory");
           }
-          if constexpr (kSym) {
-            if (mirror) {
-              // row = tile column 8u + e, 16-bit position = lane
+          if (mirror) {
+            // row = tile column 8u + e, 16-bit position = lane
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int rr = 8 * u + e;
-                const uint32_t dst = slot + L::kBoxBytes + rr * 64 +
-                                     (((lane >> 3) ^ ((rr >> 1) & 3)) << 4) + (lane & 7) * 2;
-                const uint16_t hv = static_cast<uint16_t>(e & 1 ? o[e >> 1] >> 16 : o[e >> 1]);
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst), "h"(hv) : "memory");
-              }
+            for (int e = 0; e < 8; ++e) {
+              const int rr = 8 * u + e;
+              const uint32_t dst = slot + L::kBoxBytes + rr * 64 +
+                                   (((lane >> 3) ^ ((rr >> 1) & 3)) << 4) + (lane & 7) * 2;
+              const uint16_t hv = static_cast<uint16_t>(e & 1 ? o[e >> 1] >> 16 : o[e >> 1]);
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst), "h"(hv) : "memory");
             }
           }
         }
@@ -499,31 +497,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           tma_store_2d(&maps.out[j], slot, x0 + gi * 32, y0);
-          if constexpr (MODE == kUpdate) tma_store_2d(&maps.lo[j], slot + L::kBoxBytes, x0 + gi * 32, y0);
-          if constexpr (kSym) {
-            if (mirror) tma_store_2d(&maps.out[j], slot + L::kBoxBytes, y0, x0 + gi * 32);
-          }
+          if (split) tma_store_2d(&maps.lo[j], slot + L::kBoxBytes, x0 + gi * 32, y0);
+          // (a box of padding columns has no mirror image)
+          if (mirror && x0 + gi * 32 < rows)
+            tma_store_2d(&maps.out[j], slot + L::kBoxBytes, y0, x0 + gi * 32);
           bulk_commit_group();
         }
-        if constexpr (kHasC) {
-          if (gi + L::kAhead < boxes) load_c(gi + L::kAhead);
-        }
       }
-      if (!ok) break;
       // every TMEM read of this tile has landed
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty_leader0 + 8u * tb);
     }
-    if (lane == 0) {
-      for (; used < loads; ++used) {     // after an expired wait: let the copies land
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(slot_bar(ew, used % L::kSlots), (used / L::kSlots) & 1u) &&
-               globaltimer_ns() - t0 < kWaitLimitNs) {
-        }
-      }
-      bulk_wait_group_all();
-    }
+    if (lane == 0) bulk_wait_group_all();
   }
 
   tc_fence_before();
@@ -539,8 +525,9 @@ constexpr int kNormBlocks = 128;       // partial sums of squares per job
 constexpr int kSplitThreads = 256;
 
 struct InJob {
-  const void* g;        // bf16 or fp32, count elements (a multiple of 256)
-  int64_t count;
+  const void* g;        // bf16 or fp32 [rows, cols]
+  int64_t count;        // rows * cols, a multiple of 256
+  int cols, pitch;      // hi and lo have rows of `pitch` elements
   double* part;         // [kNormBlocks]
   uint16_t* hi;
   uint16_t* lo;
@@ -601,10 +588,17 @@ __global__ void __launch_bounds__(kSplitThreads) ns_split_kernel(const __grid_co
   const InJob& j = a.job[blockIdx.y];
   const double ss = block_sum(threadIdx.x < kNormBlocks ? j.part[threadIdx.x] : 0.0, buf);
   const double scale = kXScale / (sqrt(ss) + static_cast<double>(a.eps));
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kSplitThreads + threadIdx.x) * 8; i < j.count;
+  const int64_t total = j.count / j.cols * j.pitch;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kSplitThreads + threadIdx.x) * 8; i < total;
        i += static_cast<int64_t>(gridDim.x) * kSplitThreads * 8) {
-    float v[8];
-    load_g8(j.g, a.g_f32, i, v);
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (j.pitch == j.cols) {
+      load_g8(j.g, a.g_f32, i, v);
+    } else {
+      const int64_t row = i / j.pitch;
+      const int col = static_cast<int>(i - row * j.pitch);
+      if (col < j.cols) load_g8(j.g, a.g_f32, row * j.cols + col, v);
+    }
     uint32_t h[4], l[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

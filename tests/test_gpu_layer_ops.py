@@ -223,6 +223,49 @@ def test_newton_schulz(shapes, steps, f32):
     assert float((alone.double() - ref).norm()) <= R.ns_tolerance(steps) * float(ref.norm())
 
 
+@pytest.mark.parametrize("shapes", [["1040x2064"], ["2320x1040", "512x272", "1040x1040"],
+                                    ["1136x1712", "16x48", "1712x1136"]],
+                         ids=lambda s: "+".join(s))
+@pytest.mark.parametrize("steps", [2, 3, 5, 6, 7])
+def test_newton_schulz_pairs_of_steps(shapes, steps):
+    """Oblong matrices large enough to take some steps in pairs on their short
+    side, alone and beside matrices that do not."""
+    torch, ops = _t(), _ops()
+    gs = [_normal(tuple(int(v) for v in s.split("x")), 250 + i, 1e-3, torch.float32)
+          for i, s in enumerate(shapes)]
+    outs = ops.newton_schulz_batch(gs, steps=steps)
+    ops.fp8bw_check_device_error()
+    for g, o in zip(gs, outs):
+        ref = R.newton_schulz(g, steps, (3.4445, -4.7750, 2.0315), 1e-7)
+        assert float((o.double() - ref).norm()) <= R.ns_tolerance(steps) * float(ref.norm())
+    assert all(torch.equal(a, b) for a, b in zip(outs, ops.newton_schulz_batch(gs, steps=steps)))
+
+
+def test_newton_schulz_pairs_with_other_coefficients_and_spectra():
+    torch, ops = _t(), _ops()
+    g = _normal((1040, 2064), 260, 1e-3, torch.float32)
+    u = torch.linalg.qr(_normal((1040, 4), 261, 1.0, torch.float32))[0]
+    v = torch.linalg.qr(_normal((2064, 4), 262, 1.0, torch.float32))[0]
+    low = g + 20.0 * u @ v.t()               # four directions some 250 times the rest
+    for m, coeffs in ((low, (3.4445, -4.7750, 2.0315)), (g, (1.5, -0.5, 0.0)),
+                      (g, (2.0, -1.5, 0.5)), (0.01 * g, (6.0, -9.0, 4.0))):
+        ref = R.newton_schulz(m, 5, coeffs, 1e-7)
+        got = ops.newton_schulz(m, coeffs=coeffs)
+        if float(ref.abs().max()) > 4.0:
+            # (6, -9, 4) diverges, to 1e45: outside what the operator promises,
+            # which is a result that is not finite rather than a wrong one
+            assert not bool(torch.isfinite(got.float()).all())
+            continue
+        assert float((got.double() - ref).norm()) <= R.ns_tolerance(5) * float(ref.norm())
+    # a steep polynomial, whose product of two steps would not fit
+    steep = (8.1566, -22.4833, 15.8789)
+    ref = R.newton_schulz(g, 2, steep, 1e-7)
+    got = ops.newton_schulz(g, steps=2, coeffs=steep)
+    # B's norm is up to 5.7 here instead of 2.8, and a step multiplies by up to
+    # 8.2 instead of 3.4
+    assert float((got.double() - ref).norm()) <= 2 * R.ns_tolerance(2) * float(ref.norm())
+
+
 def test_newton_schulz_singular_values_and_extremes():
     torch, ops = _t(), _ops()
     g = _normal((256, 640), 300, 1e-3, torch.float32)
