@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
   }
   if (a.q == nullptr) return;
   float qs, s;
-  scale_of<POW2>(m[0] * rstd, qs, s);
+  scale_near<POW2>(m[0] * rstd, qs, s);
   const float f = qs * rstd;
   const bool out = row < a.row_end;
   const int64_t first = (t & ~15) + mine * tpr;       // first chunk of this lane's group
@@ -245,7 +245,7 @@ struct NormColArgs {
   CodesOut out;
 };
 
-using NormRing = TileRing<1, 5>;
+using NormRing = TileRing<1, 3>;
 struct NormColSmem {
   static constexpr int kEmit = (NormRing::kBytes + 127) / 128 * 128;
   static constexpr int kAlloc = kEmit + TileEmit<1, false, false>::kBytes + 128;
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return;
   }
   const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  RingReader reader(ring);
   TileEmit<1, false, POW2> emit(smem + NormColSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = tile_of(i);
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
     for (int p = 0; p < 8; ++p) rs[p] = r0 + p < a.rows ? __ldg(a.rstd + r0 + p) : 0.0f;
     float y[1][8][4];
-    const uint8_t* in = ring.wait(i, 0);
+    const uint8_t* in = reader.next(0);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       read4(in, p, y[0][p]);
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fmul2(y[0][p][j], y[0][p][j + 1], y[0][p][j], y[0][p][j + 1], g[j], g[j + 1]);
       }
     }
-    ring.release(i);
+    reader.release();
     emit.step(y, tr, {tc});
   }
   emit.finish();

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kGluRowThreads) swiglu_row_kernel(const GluRow
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float qs, s;
-  scale_of<POW2>(m, qs, s);
+  scale_near<POW2>(m, qs, s);
   if (row < a.rows_pad && c < a.f) {
     *reinterpret_cast<uint2*>(a.q + row * a.f + c) =
         make_uint2(encode4(y[0], y[1], y[2], y[3], qs), encode4(y[4], y[5], y[6], y[7], qs));
@@ -96,15 +96,19 @@ __device__ __forceinline__ int tiles_of_block(int num_tiles) {
          static_cast<int>(gridDim.x);
 }
 
-using GluFwdRing = TileRing<2, 6>;      // gate, up
+// Two blocks per SM, each with the inputs of one step in its ring: they compute
+// while the other waits (114 us at 16384 x 6144; one block with three steps'
+// inputs: 118).
+constexpr int kGluFwdBlocks = 2;
+using GluFwdRing = TileRing<2, 2>;      // gate, up
 struct GluFwdSmem {
   static constexpr int kEmit = (GluFwdRing::kBytes + 127) / 128 * 128;
   static constexpr int kAlloc = kEmit + TileEmit<1, true, false>::kBytes + 128;
-  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+  static_assert(kGluFwdBlocks * kAlloc <= 227 * 1024, "shared memory budget");
 };
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(kTileThreads, kGluFwdBlocks)
     swiglu_tile_kernel(const __grid_constant__ CUtensorMap map_g,
                        const __grid_constant__ CUtensorMap map_u, const GluTileArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -127,12 +131,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     });
     return;
   }
+  RingReader reader(ring);
   TileEmit<1, true, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
     float y[1][8][4];
-    const uint8_t* gate = ring.wait(i, 0);
-    const uint8_t* up = ring.wait(i, 1);
+    const uint8_t* gate = reader.next(0);
+    const uint8_t* up = reader.next(1);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       float g[4], u[4];
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; j += 2) glu2(g + j, u + j, &y[0][p][j]);
     }
-    ring.release(i);
+    reader.release();
     emit.step(y, tile / a.tiles_c, {tile % a.tiles_c});
   }
   emit.finish();
@@ -196,14 +201,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     });
     return;
   }
+  RingReader reader(ring);
   TileEmit<2, true, POW2> emit(smem + GluBwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
     const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
     float y[2][8][4];
-    const uint8_t* gate = ring.wait(i, 0);
-    const uint8_t* up = ring.wait(i, 1);
-    const uint8_t* da = ring.wait(i, 2);
+    const uint8_t* gate = reader.next(0);
+    const uint8_t* up = reader.next(1);
+    const uint8_t* da = reader.next(2);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       float g[4], u[4], d[4];
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; j += 2) glu_grad2(g + j, u + j, d + j, &y[0][p][j], &y[1][p][j]);
     }
-    ring.release(i);
+    reader.release();
     emit.step(y, tr, {tc, tc + a.tiles_c});
   }
   emit.finish();

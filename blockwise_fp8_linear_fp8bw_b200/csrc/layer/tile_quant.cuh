@@ -58,6 +58,24 @@ __device__ __forceinline__ float max3_abs(float m, float a, float b) {
   return r;
 }
 
+// scale_of for the fused kernels: the reciprocals are within 2 ulp instead of
+// correctly rounded (two IEEE divisions cost some 40 instructions and their
+// latency, in every step). With amax / 448 to 1 ulp and 448 / amax to 2, amax still
+// encodes as 448, and other codes differ only for values within 2^-21 of a tie.
+template <bool POW2>
+__device__ __forceinline__ void scale_near(float amax, float& qscale, float& s) {
+  if constexpr (POW2) {
+    group_scale_pow2(amax, qscale, s);
+  } else {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax));
+    r *= 448.0f;
+    const bool none = !isfinite(r) || amax == 0.0f;
+    qscale = none ? 1.0f : r;
+    s = none ? 1.0f : amax * (1.0f / 448.0f);
+  }
+}
+
 // Largest |v| of the warp, in every lane.
 __device__ __forceinline__ float warp_max_abs(float v) {
   float r;
@@ -122,9 +140,9 @@ struct TileEmit {
     col_at = static_cast<int64_t>(t >> 3) * o.rows + (t & 7) * 16;
   }
 
-  // What is left of the tensor from tile index i on, at most a tile.
+  // What is left of the tensor from tile index i on (sizes fit 31 bits).
   __device__ __forceinline__ static int left(int64_t size, int i) {
-    return static_cast<int>(min(static_cast<int64_t>(kTile), size - static_cast<int64_t>(i) * kTile));
+    return static_cast<int>(size) - i * kTile;
   }
 
   __device__ __forceinline__ void step(const float (&y)[NOUT][8][4], int tr, const int (&tc)[NOUT]) {
@@ -152,7 +170,7 @@ struct TileEmit {
 #pragma unroll
       for (int w = 0; w < 16; w += 2) m = max3_abs(m, r[w * kTile], r[(w + 1) * kTile]);
       float qs, s;
-      scale_of<POW2>(m, qs, s);
+      scale_near<POW2>(m, qs, s);
       colq[t] = qs;
       const int c = NOUT == 1 || n == 0 ? tc[0] : tc[NOUT - 1];
       if (k < left(out.cols, c))
@@ -221,7 +239,7 @@ struct TileEmit {
       if ((lane & 7) == p) mine = m;
     }
     float qs, s;
-    scale_of<POW2>(mine, qs, s);
+    scale_near<POW2>(mine, qs, s);
     // rows is a multiple of 16: the warp's 8 rows are all in or all out
     const bool rin = rb * 8 < left(out.rows, tr);
     const int64_t r0 = static_cast<int64_t>(tr) * kTile;
@@ -288,19 +306,35 @@ struct TileRing {
       }
     }
   }
-  // The working warps: wait for input n of step i (nullptr after an expired
-  // wait); release it once it has been read.
-  __device__ __forceinline__ const uint8_t* wait(int i, int n) const {
-    const int k = i * NIN + n;
-    return mbar_wait(full(k % SLOTS), (k / SLOTS) & 1, abort, kErrTimeoutTma)
-               ? base + (k % SLOTS) * kTileBytes
-               : nullptr;
+};
+
+// Where a working warp is in its block's ring.
+template <int NIN, int SLOTS>
+struct RingReader {
+  const TileRing<NIN, SLOTS>& ring;
+  int slot = 0;
+  uint32_t phase = 0;
+  uint32_t taken[NIN];
+
+  __device__ __forceinline__ explicit RingReader(const TileRing<NIN, SLOTS>& r) : ring(r) {}
+  // Wait for the next input (nullptr after an expired wait) ...
+  __device__ __forceinline__ const uint8_t* next(int n) {
+    const uint8_t* p = mbar_wait(ring.full(slot), phase, ring.abort, kErrTimeoutTma)
+                           ? ring.base + slot * kTileBytes
+                           : nullptr;
+    taken[n] = ring.empty(slot);
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return p;
   }
-  __device__ __forceinline__ void release(int i) const {
+  // ... and release a step's inputs once they have been read.
+  __device__ __forceinline__ void release() const {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int n = 0; n < NIN; ++n) mbar_arrive(empty((i * NIN + n) % SLOTS));
+      for (int n = 0; n < NIN; ++n) mbar_arrive(taken[n]);
     }
   }
 };
