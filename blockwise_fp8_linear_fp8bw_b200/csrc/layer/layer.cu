@@ -409,7 +409,7 @@ int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t row
     const GluRaggedArgs r{gu, da, rows, f, a};
     const int tiles = a.tiles_r * a.tiles_c;
     return launched(launch_kernel(swiglu_bwd_ragged_kernel<POW2>,
-                                  dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kWorkThreads),
+                                  dim3(std::min(tiles, 2 * dev.sm_count)), dim3(kTileThreads),
                                   TileEmit<1, true, false>::kBytes + 128, cs, r));
   }
   CUtensorMap mg, mu, md;

@@ -245,7 +245,8 @@ struct NormColArgs {
   CodesOut out;
 };
 
-using NormRing = TileRing<1, 3>;
+constexpr int kNormSlots = 3;
+using NormRing = TileRing<1, kNormSlots>;
 struct NormColSmem {
   static constexpr int kEmit = (NormRing::kBytes + 127) / 128 * 128;
   static constexpr int kAlloc = kEmit + TileEmit<1, false, false>::kBytes + 128;
@@ -256,8 +257,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     norm_col_kernel(const __grid_constant__ CUtensorMap map_h, const NormColArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const NormRing ring(smem);
   const int num_tiles = a.tiles_r * a.tiles_c;
+  const int count = tiles_of_block(num_tiles);
+  NormRing ring(smem, count);
   if (threadIdx.x == 0) {
     ring.init();
     prefetch_tmap(&map_h);
@@ -265,19 +267,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  const int count = (num_tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-                    static_cast<int>(gridDim.x);
   // last rows first: they are the most recently written, and still in L2
   auto tile_of = [&](int i) { return num_tiles - 1 - static_cast<int>(blockIdx.x + i * gridDim.x); };
-  if (threadIdx.x >= kWorkThreads) {
-    ring.produce(count, [&](int i, int, uint32_t dst, uint32_t bar) {
-      const int tile = tile_of(i);
-      tma_load_2d(dst, &map_h, bar, (tile % a.tiles_c) * kTile, (a.tr0 + tile / a.tiles_c) * kTile);
-    });
-    return;
-  }
+  auto load = [&](int i, int, uint32_t dst, uint32_t bar) {
+    const int tile = tile_of(i);
+    tma_load_2d(dst, &map_h, bar, (tile % a.tiles_c) * kTile, (a.tr0 + tile / a.tiles_c) * kTile);
+  };
+  if (threadIdx.x == 0) ring.fill(kNormSlots, load);
   const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  RingReader reader(ring);
   TileEmit<1, false, POW2> emit(smem + NormColSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = tile_of(i);
@@ -289,7 +286,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
     for (int p = 0; p < 8; ++p) rs[p] = r0 + p < a.rows ? __ldg(a.rstd + r0 + p) : 0.0f;
     float y[1][8][4];
-    const uint8_t* in = reader.next(0);
+    const uint8_t* in = ring.next();
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       read4(in, p, y[0][p]);
@@ -299,10 +296,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fmul2(y[0][p][j], y[0][p][j + 1], y[0][p][j], y[0][p][j + 1], g[j], g[j + 1]);
       }
     }
-    reader.release();
-    emit.step(y, tr, {tc});
+    emit.step(y, tr, {tc}, [&] {
+      if (threadIdx.x == 0) ring.fill(1, load);
+    });
   }
   emit.finish();
+  if (threadIdx.x == 0) ring.drain();
 }
 
 // ---------------------------------------------------------------- backward

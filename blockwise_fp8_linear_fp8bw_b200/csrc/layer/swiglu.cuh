@@ -90,17 +90,11 @@ struct GluTileArgs {
   CodesOut out;
 };
 
-// The block's tiles: blockIdx.x, blockIdx.x + gridDim.x, ...
-__device__ __forceinline__ int tiles_of_block(int num_tiles) {
-  return (num_tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-         static_cast<int>(gridDim.x);
-}
-
 // Two blocks per SM, each with the inputs of one step in its ring: they compute
 // while the other waits (114 us at 16384 x 6144; one block with three steps'
 // inputs: 118).
-constexpr int kGluFwdBlocks = 2;
-using GluFwdRing = TileRing<2, 2>;      // gate, up
+constexpr int kGluFwdBlocks = 2, kGluFwdSlots = 2;
+using GluFwdRing = TileRing<2, kGluFwdSlots>;      // gate, up
 struct GluFwdSmem {
   static constexpr int kEmit = (GluFwdRing::kBytes + 127) / 128 * 128;
   static constexpr int kAlloc = kEmit + TileEmit<1, true, false>::kBytes + 128;
@@ -113,7 +107,8 @@ __global__ void __launch_bounds__(kTileThreads, kGluFwdBlocks)
                        const __grid_constant__ CUtensorMap map_u, const GluTileArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const GluFwdRing ring(smem);
+  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
+  GluFwdRing ring(smem, count);
   if (threadIdx.x == 0) {
     ring.init();
     prefetch_tmap(&map_g);
@@ -122,22 +117,18 @@ __global__ void __launch_bounds__(kTileThreads, kGluFwdBlocks)
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
-  if (threadIdx.x >= kWorkThreads) {
-    ring.produce(count, [&](int i, int n, uint32_t dst, uint32_t bar) {
-      const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
-      tma_load_2d(dst, n == 0 ? &map_g : &map_u, bar, (tile % a.tiles_c) * kTile,
-                  (tile / a.tiles_c) * kTile);
-    });
-    return;
-  }
-  RingReader reader(ring);
+  auto load = [&](int i, int n, uint32_t dst, uint32_t bar) {
+    const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
+    tma_load_2d(dst, n == 0 ? &map_g : &map_u, bar, (tile % a.tiles_c) * kTile,
+                (tile / a.tiles_c) * kTile);
+  };
+  if (threadIdx.x == 0) ring.fill(kGluFwdSlots, load);
   TileEmit<1, true, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
     float y[1][8][4];
-    const uint8_t* gate = reader.next(0);
-    const uint8_t* up = reader.next(1);
+    const uint8_t* gate = ring.next();
+    const uint8_t* up = ring.next();
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       float g[4], u[4];
@@ -146,10 +137,12 @@ __global__ void __launch_bounds__(kTileThreads, kGluFwdBlocks)
 #pragma unroll
       for (int j = 0; j < 4; j += 2) glu2(g + j, u + j, &y[0][p][j]);
     }
-    reader.release();
-    emit.step(y, tile / a.tiles_c, {tile % a.tiles_c});
+    emit.step(y, tile / a.tiles_c, {tile % a.tiles_c}, [&] {
+      if (threadIdx.x == 0) ring.fill(2, load);
+    });
   }
   emit.finish();
+  if (threadIdx.x == 0) ring.drain();
 }
 
 // Two elements of the backward pass.
@@ -168,7 +161,8 @@ __device__ __forceinline__ void glu_grad2(const float* g, const float* u, const 
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
 // two halves): gate, up and da tiles in, a dgate and a dup tile out.
-using GluBwdRing = TileRing<3, 5>;
+constexpr int kGluBwdSlots = 5;
+using GluBwdRing = TileRing<3, kGluBwdSlots>;
 struct GluBwdSmem {
   static constexpr int kEmit = (GluBwdRing::kBytes + 127) / 128 * 128;
   static constexpr int kAlloc = kEmit + TileEmit<2, true, false>::kBytes + 128;
@@ -182,7 +176,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                            const __grid_constant__ CUtensorMap map_da, const GluTileArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const GluBwdRing ring(smem);
+  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
+  GluBwdRing ring(smem, count);
   if (threadIdx.x == 0) {
     ring.init();
     prefetch_tmap(&map_g);
@@ -192,24 +187,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
-  if (threadIdx.x >= kWorkThreads) {
-    ring.produce(count, [&](int i, int n, uint32_t dst, uint32_t bar) {
-      const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
-      tma_load_2d(dst, n == 0 ? &map_g : n == 1 ? &map_u : &map_da, bar,
-                  (tile % a.tiles_c) * kTile, (tile / a.tiles_c) * kTile);
-    });
-    return;
-  }
-  RingReader reader(ring);
+  auto load = [&](int i, int n, uint32_t dst, uint32_t bar) {
+    const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
+    tma_load_2d(dst, n == 0 ? &map_g : n == 1 ? &map_u : &map_da, bar, (tile % a.tiles_c) * kTile,
+                (tile / a.tiles_c) * kTile);
+  };
+  if (threadIdx.x == 0) ring.fill(kGluBwdSlots, load);
   TileEmit<2, true, POW2> emit(smem + GluBwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
     const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
     float y[2][8][4];
-    const uint8_t* gate = reader.next(0);
-    const uint8_t* up = reader.next(1);
-    const uint8_t* da = reader.next(2);
+    const uint8_t* gate = ring.next();
+    const uint8_t* up = ring.next();
+    const uint8_t* da = ring.next();
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       float g[4], u[4], d[4];
@@ -219,10 +210,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; j += 2) glu_grad2(g + j, u + j, d + j, &y[0][p][j], &y[1][p][j]);
     }
-    reader.release();
-    emit.step(y, tr, {tc, tc + a.tiles_c});
+    emit.step(y, tr, {tc, tc + a.tiles_c}, [&] {
+      if (threadIdx.x == 0) ring.fill(3, load);
+    });
   }
   emit.finish();
+  if (threadIdx.x == 0) ring.drain();
 }
 
 // Backward for f no multiple of 128: the 1x128 groups of d then straddle the
@@ -237,7 +230,7 @@ struct GluRaggedArgs {
 };
 
 template <bool POW2>
-__global__ void __launch_bounds__(kWorkThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 2)
     swiglu_bwd_ragged_kernel(const GluRaggedArgs r) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
@@ -275,7 +268,7 @@ __global__ void __launch_bounds__(kWorkThreads, 2)
         }
       }
     }
-    emit.step(y, tr, {tc});
+    emit.step(y, tr, {tc}, [] {});
   }
   emit.finish();
 }

@@ -3,11 +3,10 @@
 // column-wise codes (transposed) with 128x1 scales, with the arithmetic and
 // layouts of the quantisers.
 //
-// 512 working threads: warp w owns rows 8w .. 8w+7 of the tile and lane l the
-// columns 4l .. 4l+3, so a warp holds eight whole 1x128 groups and a thread 32
-// values per tile (two tiles at once fit its registers). A 17th warp only loads:
-// it keeps a ring of input tiles filled by TMA, so reads stay in flight while
-// the others work.
+// 512 threads: warp w owns rows 8w .. 8w+7 of the tile and lane l the columns
+// 4l .. 4l+3, so a warp holds eight whole 1x128 groups and a thread 32 values per
+// tile (two tiles at once fit its registers). A ring of input tiles is kept
+// filled by TMA.
 #pragma once
 
 #include <cuda.h>
@@ -18,8 +17,7 @@ namespace fp8bw {
 namespace layer {
 
 constexpr int kTile = 128;
-constexpr int kWorkThreads = 512;
-constexpr int kTileThreads = kWorkThreads + 32;
+constexpr int kTileThreads = 512;
 constexpr int kTileBytes = kTile * kTile * 2;   // one bf16 tile
 
 __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
@@ -30,6 +28,12 @@ __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// The block's tiles: blockIdx.x, blockIdx.x + gridDim.x, ...
+__device__ __forceinline__ int tiles_of_block(int num_tiles) {
+  return (num_tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+         static_cast<int>(gridDim.x);
 }
 
 // Four values as E4M3 (round to nearest even, saturating), a in the low byte.
@@ -94,11 +98,6 @@ __device__ __forceinline__ void fadd2(float& p0, float& p1, float x0, float x1, 
       : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
 }
 
-// A barrier of the working threads.
-__device__ __forceinline__ void work_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kWorkThreads) : "memory");
-}
-
 // Where codes and scales go (row-wise ones may be unused).
 struct CodesOut {
   uint8_t* q;          // [rows][cols]
@@ -117,7 +116,7 @@ __device__ __forceinline__ int emit_t_offset(int k, int u) {
 }
 
 // Writes the codes of NOUT tiles per step, all of row tile tr, from the 8x4
-// values of each working thread; entries outside the tensor must be zero. Column
+// values of each thread; entries outside the tensor must be zero. Column
 // scales need the whole tile, so a step has two barriers. To have work between
 // them, the transposed codes of a step leave shared memory during the next one:
 // between the barriers lie this step's row codes, the last step's transposed
@@ -145,7 +144,11 @@ struct TileEmit {
     return static_cast<int>(size) - i * kTile;
   }
 
-  __device__ __forceinline__ void step(const float (&y)[NOUT][8][4], int tr, const int (&tc)[NOUT]) {
+  // `freed()` runs after the first barrier: every thread is past reading the
+  // inputs that y came from.
+  template <typename Freed>
+  __device__ __forceinline__ void step(const float (&y)[NOUT][8][4], int tr,
+                                       const int (&tc)[NOUT], Freed&& freed) {
     const int t = threadIdx.x, rb = t >> 5, lane = t & 31;
     float* red = reinterpret_cast<float*>(smem + kRed);
     float* colq = reinterpret_cast<float*>(smem + kColQ);
@@ -162,7 +165,8 @@ struct TileEmit {
       *reinterpret_cast<float4*>(red + (n * 16 + rb) * kTile + lane * 4) =
           make_float4(m[0], m[1], m[2], m[3]);
     }
-    work_sync();
+    __syncthreads();
+    freed();
     if (t < NOUT * kTile) {
       const int n = t >> 7, k = t & 127;
       const float* r = red + n * 16 * kTile + k;
@@ -181,7 +185,7 @@ struct TileEmit {
 #pragma unroll
       for (int n = 0; n < NOUT; ++n) write_rows(y[n], tr, tc[n]);
     }
-    work_sync();
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NOUT; ++n) {
       uint8_t* T = smem + kT + n * kTile * kTile;
@@ -205,7 +209,7 @@ struct TileEmit {
   // After the last step.
   __device__ __forceinline__ void finish() {
     if (last_tr < 0) return;
-    work_sync();
+    __syncthreads();
     write_transposed();
   }
 
@@ -220,7 +224,7 @@ struct TileEmit {
       uint8_t* dst = out.q_t + static_cast<int64_t>(last_tc[n]) * kTile * out.rows +
                      static_cast<int64_t>(last_tr) * kTile + col_at;
 #pragma unroll
-      for (int k0 = 0; k0 < kTile; k0 += kWorkThreads / 8) {
+      for (int k0 = 0; k0 < kTile; k0 += kTileThreads / 8) {
         const uint2 lo = *reinterpret_cast<const uint2*>(T + emit_t_offset(k0 + kk, 2 * ch));
         const uint2 hi = *reinterpret_cast<const uint2*>(T + emit_t_offset(k0 + kk, 2 * ch + 1));
         if (rin && k0 + kk < cols)
@@ -257,84 +261,63 @@ struct TileEmit {
 };
 
 // ---------------------------------------------------------------- input ring
-// A ring of SLOTS bf16 tiles, filled by the 17th warp and read by the 16 working
-// ones; the i-th step of a block takes the NIN tiles i*NIN .. i*NIN+NIN-1 of the
-// sequence. Every wait is bounded. After an expired one the working warps go on
-// through their remaining steps (the abort flag ends every further wait), so
-// that all of them meet at every barrier.
+// A ring of SLOTS bf16 tiles, filled by thread 0 and read by all; the i-th step
+// of a block takes the NIN tiles i*NIN .. i*NIN+NIN-1 of its sequence. Every wait
+// is bounded. After an expired one the threads go on through their remaining
+// steps (the abort flag ends every further wait), so that all of them meet at
+// every barrier.
 template <int NIN, int SLOTS>
 struct TileRing {
-  static constexpr int kBar = SLOTS * kTileBytes;            // full, empty
-  static constexpr int kBytes = kBar + 2 * SLOTS * 8 + 16;
+  static_assert(SLOTS >= NIN, "a step's inputs fit the ring");
+  static constexpr int kBar = SLOTS * kTileBytes;
+  static constexpr int kBytes = kBar + SLOTS * 8 + 16;
 
   uint8_t* base;
   uint32_t bar;
   volatile uint32_t* abort;
+  int slot = 0;              // next to read ...
+  uint32_t phase = 0;
+  int fill_slot = 0, filled = 0, total;      // ... and to fill (thread 0)
 
-  __device__ __forceinline__ explicit TileRing(uint8_t* p)
+  __device__ __forceinline__ TileRing(uint8_t* p, int steps)
       : base(p), bar(smem_u32(p) + kBar),
-        abort(reinterpret_cast<volatile uint32_t*>(p + kBar + 2 * SLOTS * 8)) {}
-  __device__ __forceinline__ uint32_t full(int s) const { return bar + 8u * s; }
-  __device__ __forceinline__ uint32_t empty(int s) const { return bar + 8u * (SLOTS + s); }
+        abort(reinterpret_cast<volatile uint32_t*>(p + kBar + SLOTS * 8)), total(steps * NIN) {}
   __device__ __forceinline__ void init() const {      // one thread
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kWorkThreads / 32);
-    }
+    for (int s = 0; s < SLOTS; ++s) mbar_init(bar + 8u * s, 1);
     *abort = 0u;
     fence_mbar_init();
   }
-  // The loading warp: `fill(i, n, dst, bar)` issues the load of the n-th input
-  // of step i, for i in [0, steps).
-  template <typename Fill>
-  __device__ __forceinline__ void produce(int steps, Fill&& fill) const {
-    if ((threadIdx.x & 31) != 0) return;
-    const int total = steps * NIN;
-    int i = 0;
-    for (; i < total; ++i) {
-      const int s = i % SLOTS;
-      if (!mbar_wait(empty(s), ((i / SLOTS) & 1) ^ 1, abort, kErrTimeoutTma)) break;
-      mbar_arrive_expect_tx(full(s), kTileBytes);
-      fill(i / NIN, i % NIN, smem_u32(base) + s * kTileBytes, full(s));
-    }
-    // the block's shared memory must outlive the copies into it: wait for the
-    // last ones even if their readers have given up
-    for (int k = i > SLOTS ? i - SLOTS : 0; k < i; ++k) {
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(full(k % SLOTS), (k / SLOTS) & 1) &&
-             globaltimer_ns() - t0 < kWaitLimitNs) {
-      }
+  // Thread 0: load up to `count` tiles more; `load(i, n, dst, bar)` issues the
+  // load of input n of step i. Their slots must be free.
+  template <typename Load>
+  __device__ __forceinline__ void fill(int count, Load&& load) {
+    for (int k = 0; k < count && filled < total; ++k, ++filled) {
+      const uint32_t b = bar + 8u * fill_slot;
+      mbar_arrive_expect_tx(b, kTileBytes);
+      load(filled / NIN, filled % NIN, smem_u32(base) + fill_slot * kTileBytes, b);
+      if (++fill_slot == SLOTS) fill_slot = 0;
     }
   }
-};
-
-// Where a working warp is in its block's ring.
-template <int NIN, int SLOTS>
-struct RingReader {
-  const TileRing<NIN, SLOTS>& ring;
-  int slot = 0;
-  uint32_t phase = 0;
-  uint32_t taken[NIN];
-
-  __device__ __forceinline__ explicit RingReader(const TileRing<NIN, SLOTS>& r) : ring(r) {}
-  // Wait for the next input (nullptr after an expired wait) ...
-  __device__ __forceinline__ const uint8_t* next(int n) {
-    const uint8_t* p = mbar_wait(ring.full(slot), phase, ring.abort, kErrTimeoutTma)
-                           ? ring.base + slot * kTileBytes
+  // The next input, or nullptr after an expired wait.
+  __device__ __forceinline__ const uint8_t* next() {
+    const uint8_t* p = mbar_wait(bar + 8u * slot, phase, abort, kErrTimeoutTma)
+                           ? base + slot * kTileBytes
                            : nullptr;
-    taken[n] = ring.empty(slot);
     if (++slot == SLOTS) {
       slot = 0;
       phase ^= 1u;
     }
     return p;
   }
-  // ... and release a step's inputs once they have been read.
-  __device__ __forceinline__ void release() const {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int n = 0; n < NIN; ++n) mbar_arrive(taken[n]);
+  // Thread 0, after the last step: the block's shared memory must outlive the
+  // copies into it, even if their readers gave up (every copy has then been
+  // waited for already, and these return at once).
+  __device__ __forceinline__ void drain() const {
+    for (int k = filled > SLOTS ? filled - SLOTS : 0; k < filled; ++k) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar + 8u * (k % SLOTS), (k / SLOTS) & 1) &&
+             globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
     }
   }
 };
