@@ -378,9 +378,8 @@ int swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, flo
   if (st != FP8BW_OK) return st;
   const GluTileArgs a{static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
                       CodesOut{q, s, q_t, s_t, rp, f}};
-  const int tiles = a.tiles_r * a.tiles_c;
-  return launched(launch_kernel(swiglu_tile_kernel<POW2>,
-                                dim3(std::min(tiles, kGluFwdBlocks * dev.sm_count)),
+  const int tiles = a.tiles_r * ((a.tiles_c + 1) / 2);     // pairs
+  return launched(launch_kernel(swiglu_tile_kernel<POW2>, dim3(std::min(tiles, dev.sm_count)),
                                 dim3(kTileThreads), GluFwdSmem::kAlloc, cs, mg, mu, a));
 }
 

@@ -90,55 +90,61 @@ struct GluTileArgs {
   CodesOut out;
 };
 
-// Two blocks per SM, each with the inputs of one step in its ring: they compute
-// while the other waits (114 us at 16384 x 6144; one block with three steps'
-// inputs: 118).
-constexpr int kGluFwdBlocks = 2, kGluFwdSlots = 2;
-using GluFwdRing = TileRing<2, kGluFwdSlots>;      // gate, up
+// Forward: two tiles per step, half the columns apart, so that the barriers of a
+// step stand beside twice the work (113 us at 16384 x 6144 with one tile per
+// step, in two blocks per SM).
+constexpr int kGluFwdSlots = 6;
+using GluFwdRing = TileRing<4, kGluFwdSlots>;      // gate, up, twice
 struct GluFwdSmem {
   static constexpr int kEmit = (GluFwdRing::kBytes + 127) / 128 * 128;
-  static constexpr int kAlloc = kEmit + TileEmit<1, true, false>::kBytes + 128;
-  static_assert(kGluFwdBlocks * kAlloc <= 227 * 1024, "shared memory budget");
+  static constexpr int kAlloc = kEmit + TileEmit<2, true, false>::kBytes + 128;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, kGluFwdBlocks)
+__global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_tile_kernel(const __grid_constant__ CUtensorMap map_g,
                        const __grid_constant__ CUtensorMap map_u, const GluTileArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align128(smem_raw);
-  const int count = tiles_of_block(a.tiles_r * a.tiles_c);
+  const int half = (a.tiles_c + 1) / 2;
+  const int count = tiles_of_block(a.tiles_r * half);
   GluFwdRing ring(smem, count);
   if (threadIdx.x == 0) {
     ring.init();
     prefetch_tmap(&map_g);
     prefetch_tmap(&map_u);
   }
+  TileEmit<2, true, POW2>::init(smem + GluFwdSmem::kEmit);
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
   auto load = [&](int i, int n, uint32_t dst, uint32_t bar) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
-    tma_load_2d(dst, n == 0 ? &map_g : &map_u, bar, (tile % a.tiles_c) * kTile,
-                (tile / a.tiles_c) * kTile);
+    // (a second tile past the end reads zeros)
+    const int tc = tile % half + (n >= 2 ? half : 0);
+    tma_load_2d(dst, n % 2 == 0 ? &map_g : &map_u, bar, tc * kTile, (tile / half) * kTile);
   };
   if (threadIdx.x == 0) ring.fill(kGluFwdSlots, load);
-  TileEmit<1, true, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
+  TileEmit<2, true, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
-    float y[1][8][4];
-    const uint8_t* gate = ring.next();
-    const uint8_t* up = ring.next();
+    float y[2][8][4];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      float g[4], u[4];
-      read4(gate, p, g);
-      read4(up, p, u);
+    for (int n = 0; n < 2; ++n) {
+      const uint8_t* gate = ring.next();
+      const uint8_t* up = ring.next();
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) glu2(g + j, u + j, &y[0][p][j]);
+      for (int p = 0; p < 8; ++p) {
+        float g[4], u[4];
+        read4(gate, p, g);
+        read4(up, p, u);
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) glu2(g + j, u + j, &y[n][p][j]);
+      }
     }
-    emit.step(y, tile / a.tiles_c, {tile % a.tiles_c}, [&] {
-      if (threadIdx.x == 0) ring.fill(2, load);
+    emit.step(y, tile / half, {tile % half, tile % half + half}, [&] {
+      if (threadIdx.x == 0) ring.fill(4, load);
     });
   }
   emit.finish();
@@ -161,7 +167,7 @@ __device__ __forceinline__ void glu_grad2(const float* g, const float* u, const 
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
 // two halves): gate, up and da tiles in, a dgate and a dup tile out.
-constexpr int kGluBwdSlots = 5;
+constexpr int kGluBwdSlots = 6;
 using GluBwdRing = TileRing<3, kGluBwdSlots>;
 struct GluBwdSmem {
   static constexpr int kEmit = (GluBwdRing::kBytes + 127) / 128 * 128;
@@ -184,6 +190,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tmap(&map_u);
     prefetch_tmap(&map_da);
   }
+  TileEmit<2, true, POW2>::init(smem + GluBwdSmem::kEmit);
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
@@ -237,6 +244,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const GluTileArgs& a = r.t;
   const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int num_tiles = a.tiles_r * a.tiles_c;
+  TileEmit<1, true, POW2>::init(smem);
+  __syncthreads();
   launch_dependents();
   grid_dependency_wait();
   TileEmit<1, true, POW2> emit(smem, a.out);
