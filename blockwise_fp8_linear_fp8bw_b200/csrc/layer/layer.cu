@@ -282,13 +282,13 @@ struct BwdPlan {
   int64_t blocks, parts;
 };
 
-// The fewest chunks per thread that fit a row into 512 threads; four rows (or
-// four chunks) per thread and iteration, to have the loads in flight.
+// The fewest chunks per thread that fit a row into 512 threads; two rows (or two
+// chunks) per thread and iteration, the next ones loading meanwhile.
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   BwdPlan p;
   const int64_t chunks = cols / 8;
   p.v = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
-  p.r = p.v >= 4 ? 1 : 4 / p.v;
+  p.r = p.v == 1 ? 2 : 1;
   p.tpr = threads_per_row(chunks, p.v);
   p.groups = std::max(1, 256 / std::max(p.tpr, 1));
   p.blocks = std::min<int64_t>(kBwdMaxBlocks, cdiv(rows, static_cast<int64_t>(p.groups) * p.r));
@@ -326,8 +326,8 @@ int rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd, c
   NormBwdArgs a{dy, h, rstd, gamma, gamma_is_f32 != 0, dres, rows, cols, dh,
                 static_cast<float*>(ws), p.tpr};
   using Kernel = void (*)(NormBwdArgs);
-  const Kernel kernel = p.v == 1   ? rmsnorm_bwd_kernel<1, 4>
-                        : p.v == 2 ? rmsnorm_bwd_kernel<2, 2>
+  const Kernel kernel = p.v == 1   ? rmsnorm_bwd_kernel<1, 2>
+                        : p.v == 2 ? rmsnorm_bwd_kernel<2, 1>
                         : p.v == 4 ? rmsnorm_bwd_kernel<4, 1>
                                    : rmsnorm_bwd_kernel<8, 1>;
   st = launched(launch_kernel(kernel, dim3(static_cast<unsigned>(p.blocks)),

@@ -322,12 +322,18 @@ struct NormBwdArgs {
 };
 
 // R rows x V chunks per thread and iteration; each group of tpr threads keeps
-// its columns' dgamma sums in registers over all its rows. Long rows leave no
-// registers for what the second half of an iteration needs: from V = 4 on dres
-// is loaded only there, and with V = 8 dy and h are read again (from L2).
+// its columns' dgamma sums in registers over all its rows. With
+//   s = rstd * sum_c dy gamma h   (so that mean_c(g xh) = s / cols)
+// a row is  dh = rstd (dy gamma) - (rstd^2 s / cols) h + dres: three products
+// per element before the row sum and three after it. The next iteration's rows are
+// loaded before this one's are worked on (16384 x 2048: 47 us; with twice the rows
+// per iteration and nothing ahead 50; through a shared-memory ring with a warp per
+// row 61). Long rows leave no registers for that, nor for what the second half of
+// an iteration needs: from V = 4 on dres and gamma are loaded again there, and
+// with V = 8 dy and h too (from L2).
 template <int V, int R>
 __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  constexpr bool kKeepRes = V <= 2, kKeep = V <= 4;
+  constexpr bool kKeepRes = V <= 2, kKeep = V <= 4, kAhead = V * R <= 2;
   __shared__ float part[2][R][16];
   launch_dependents();
   grid_dependency_wait();
@@ -340,19 +346,33 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
   const int chunks = static_cast<int>(a.cols >> 3);
   const float inv = __fdiv_rn(1.0f, static_cast<float>(a.cols));
   const int64_t per_block = static_cast<int64_t>(groups) * R;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto has = [&](int v) { return t + v * tpr < chunks; };
+  auto col = [&](int v) { return 8 * static_cast<int64_t>(t + v * tpr); };
 
-  float acc[V][8];
+  float acc[V][8], gamma[kKeepRes ? V : 1][8];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[v][j] = 0.0f;
+  auto load_gamma = [&](int v, float (&g)[8]) {
+    if (has(v)) {
+      load_gamma8(a.gamma, a.gamma_f32, col(v), g);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = 0.0f;
+    }
+  };
+  if constexpr (kKeepRes) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) load_gamma(v, gamma[v]);
+  }
 
   int it = 0;
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * per_block; b < a.rows;
-       b += static_cast<int64_t>(gridDim.x) * per_block, ++it) {
-    uint4 dy[R][V], h[R][V], dr[R][V];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float rs[R], dot[R];
+  uint4 dy[R][V], h[R][V], dr[R][V];
+  float rs[R];
+  auto load_rows = [&](int64_t b, uint4 (&dy)[R][V], uint4 (&h)[R][V], uint4 (&dr)[R][V],
+                       float (&rs)[R]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t row = b + r * groups + grp;
@@ -360,38 +380,46 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
       rs[r] = live ? __ldg(a.rstd + row) : 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = t + v * tpr;
-        const int64_t at = row * a.cols + 8 * static_cast<int64_t>(c);
-        const bool in = live && c < chunks;
+        const int64_t at = row * a.cols + col(v);
+        const bool in = live && has(v);
         dy[r][v] = in ? (kKeep ? ld16_stream(a.dy + at) : ld16(a.dy + at)) : zero;
         h[r][v] = in ? (kKeep ? ld16_stream(a.h + at) : ld16(a.h + at)) : zero;
         if constexpr (kKeepRes) dr[r][v] = in && a.dres != nullptr ? ld16_stream(a.dres + at) : zero;
       }
     }
+  };
+  const int64_t bstep = static_cast<int64_t>(gridDim.x) * per_block;
+  int64_t b = static_cast<int64_t>(blockIdx.x) * per_block;
+  if (b < a.rows) load_rows(b, dy, h, dr, rs);
+  for (; b < a.rows; b += bstep, ++it) {
+    uint4 ndy[R][V], nh[R][V], ndr[R][V];
+    float nrs[R], dot[R];
+    if constexpr (kAhead) {
+      if (b + bstep < a.rows) load_rows(b + bstep, ndy, nh, ndr, nrs);
+    }
+    float d0[R], d1[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) dot[r] = 0.0f;
+    for (int r = 0; r < R; ++r) d0[r] = d1[r] = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float g[8];
-      const int c = t + v * tpr;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-      if (c < chunks) load_gamma8(a.gamma, a.gamma_f32, 8 * static_cast<int64_t>(c), g);
+      if constexpr (!kKeepRes) load_gamma(v, gamma[0]);
+      const float(&g)[8] = gamma[kKeepRes ? v : 0];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float d[8], x[8];
         unpack8(dy[r][v], d);
         unpack8(h[r][v], x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float dx = d[j] * (x[j] * rs[r]);
-          acc[v][j] += dx;
-          dot[r] = fmaf(dx, g[j], dot[r]);
+        for (int j = 0; j < 8; j += 2) {
+          float p0, p1;
+          fmul2(p0, p1, d[j], d[j + 1], x[j], x[j + 1]);
+          ffma2(acc[v][j], acc[v][j + 1], p0, p1, rs[r], rs[r]);
+          ffma2(d0[r], d1[r], p0, p1, g[j], g[j + 1]);
         }
       }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) dot[r] = warp_sum(dot[r]);
+    for (int r = 0; r < R; ++r) dot[r] = warp_sum(d0[r] + d1[r]);
     if (wpr > 1) {
       float(*pt)[16] = part[it & 1];
       if ((threadIdx.x & 31) == 0) {
@@ -407,15 +435,14 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float g[8];
-      const int c = t + v * tpr;
-      if (c >= chunks) continue;
-      load_gamma8(a.gamma, a.gamma_f32, 8 * static_cast<int64_t>(c), g);
+      if (!has(v)) continue;
+      if constexpr (!kKeepRes) load_gamma(v, gamma[0]);
+      const float(&g)[8] = gamma[kKeepRes ? v : 0];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int64_t row = b + r * groups + grp;
         if (row >= a.rows) continue;
-        const int64_t at = row * a.cols + 8 * static_cast<int64_t>(c);
+        const int64_t at = row * a.cols + col(v);
         if constexpr (!kKeepRes) dr[r][v] = a.dres != nullptr ? ld16_stream(a.dres + at) : zero;
         if constexpr (!kKeep) {
           dy[r][v] = ld16_again(a.dy + at);
@@ -425,14 +452,28 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
         unpack8(dy[r][v], d);
         unpack8(h[r][v], x);
         unpack8(dr[r][v], e);
-        const float m = dot[r] * inv;
+        const float k = -(rs[r] * rs[r]) * (rs[r] * dot[r] * inv);
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          e[j] = fmaf(rs[r], fmaf(-(x[j] * rs[r]), m, d[j] * g[j]), e[j]);
-        *reinterpret_cast<uint4*>(a.dh + at) =
-            make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
-                       pack_bf16(e[6], e[7]));
+        for (int j = 0; j < 8; j += 2) {
+          float p0, p1;
+          fmul2(p0, p1, d[j], d[j + 1], g[j], g[j + 1]);
+          ffma2(e[j], e[j + 1], p0, p1, rs[r], rs[r]);
+          ffma2(e[j], e[j + 1], x[j], x[j + 1], k, k);
+          w[j >> 1] = pack_bf16(e[j], e[j + 1]);
+        }
+        *reinterpret_cast<uint4*>(a.dh + at) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        rs[r] = nrs[r];
+#pragma unroll
+        for (int v = 0; v < V; ++v) dy[r][v] = ndy[r][v], h[r][v] = nh[r][v], dr[r][v] = ndr[r][v];
+      }
+    } else if (b + bstep < a.rows) {
+      load_rows(b + bstep, dy, h, dr, rs);
     }
   }
   float* out = a.part + (static_cast<int64_t>(blockIdx.x) * groups + grp) * a.cols;
@@ -457,6 +498,7 @@ __global__ void __launch_bounds__(1024)
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
   if (c < cols)
+#pragma unroll 8
     for (int64_t p = slice; p < nparts; p += 32) s += part[p * cols + c];
   sum[slice][lane] = s;
   __syncthreads();
