@@ -244,12 +244,6 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
     a.row_end = rp;
     return norm_rows<POW2>(a, dev, cs);
   }
-  CUtensorMap map;
-  st = encode_tiles(&map, residual != nullptr ? h : x, rows, cols, 2 * cols);
-  if (st != FP8BW_OK) return st;
-  static DevicePrep prep;
-  st = allow_smem(prep, dev.ordinal, norm_col_kernel<POW2>, NormColSmem::kAlloc);
-  if (st != FP8BW_OK) return st;
   const int64_t chunk = std::max<int64_t>(128, kNormChunkBytes / (2 * cols) / 128 * 128);
   for (int64_t r0 = 0; r0 < rp; r0 += chunk) {
     a.row0 = r0;
@@ -257,18 +251,20 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
     st = norm_rows<POW2>(a, dev, cs);
     if (st != FP8BW_OK) return st;
     NormColArgs c{};
+    c.h = residual != nullptr ? h : x;
     c.rstd = rstd;
     c.gamma = gamma;
     c.gamma_f32 = a.gamma_f32;
     c.rows = rows;
+    c.rows_pad = rp;
     c.cols = cols;
     c.tr0 = static_cast<int>(r0 / 128);
     c.tiles_r = static_cast<int>(cdiv(a.row_end - r0, 128));
-    c.tiles_c = static_cast<int>(cdiv(cols, 128));
-    c.out = CodesOut{nullptr, nullptr, q_t, s_t, rp, cols};
-    const int tiles = c.tiles_r * c.tiles_c;
-    st = launched(launch_kernel(norm_col_kernel<POW2>, dim3(std::min(tiles, dev.sm_count)),
-                                dim3(kTileThreads), NormColSmem::kAlloc, cs, map, c));
+    c.tiles_c = static_cast<int>(cdiv(cols, kNormColTile));
+    c.q_t = q_t;
+    c.s_t = s_t;
+    st = launched(launch_kernel(norm_col_kernel<POW2>, dim3(c.tiles_r * c.tiles_c),
+                                dim3(kNormColThreads), 0, cs, c));
     if (st != FP8BW_OK) return st;
   }
   return FP8BW_OK;

@@ -234,77 +234,99 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
 }
 
 // ---------------------------------------------------------------- forward, column-wise
-// y of a 128x128 tile of h, from the rows' rstd, to column-wise codes.
+// y of a 128 x 64 tile of h, from the rows' rstd, to column-wise codes. Thread t of
+// 256 holds rows 8 * (t / 16) .. +7 and columns 4 * (t % 16) .. +3. A block does one
+// tile and four blocks share an SM: a tile is a chain of loads and barriers, and
+// the other blocks work meanwhile. (As steps of one 512-thread block per SM over
+// 128 x 128 tiles with a TMA ring: 63 us for both passes at 16384 x 2048.)
 struct NormColArgs {
+  const uint16_t* h;
   const float* rstd;
   const void* gamma;
   int gamma_f32;
-  int64_t rows, cols;
+  int64_t rows, rows_pad, cols;
   int tr0;                    // first row tile of this launch
   int tiles_r, tiles_c;
-  CodesOut out;
+  uint8_t* q_t;
+  float* s_t;
 };
 
-// One tile per step: two (as the gated product takes) gain 1 us of 63 at 16384 x
-// 2048 and lose 1 of 6.6 at 512 x 2048, where there are few tiles.
-constexpr int kNormSlots = 2;
-using NormRing = TileRing<1, kNormSlots>;
-struct NormColSmem {
-  static constexpr int kEmit = (NormRing::kBytes + 127) / 128 * 128;
-  static constexpr int kAlloc = kEmit + TileEmit<1, false, false>::kBytes + 128;
-};
+constexpr int kNormColTile = 64;
+constexpr int kNormColThreads = 256;
 
 template <bool POW2>
-__global__ void __launch_bounds__(kTileThreads, 1)
-    norm_col_kernel(const __grid_constant__ CUtensorMap map_h, const NormColArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align128(smem_raw);
-  const int num_tiles = a.tiles_r * a.tiles_c;
-  const int count = tiles_of_block(num_tiles);
-  NormRing ring(smem, count);
-  if (threadIdx.x == 0) {
-    ring.init();
-    prefetch_tmap(&map_h);
-  }
-  TileEmit<1, false, POW2>::init(smem + NormColSmem::kEmit);
-  __syncthreads();
+__global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const NormColArgs a) {
+  __shared__ float red[kNormColThreads / 32][kNormColTile];
+  __shared__ float colq[kNormColTile];
+  __shared__ __align__(16) uint8_t T[kNormColTile * kTile];
   launch_dependents();
   grid_dependency_wait();
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rb = t >> 4, cb = t & 15;
   // last rows first: they are the most recently written, and still in L2
-  auto tile_of = [&](int i) { return num_tiles - 1 - static_cast<int>(blockIdx.x + i * gridDim.x); };
-  auto load = [&](int i, int, uint32_t dst, uint32_t bar) {
-    const int tile = tile_of(i);
-    tma_load_2d(dst, &map_h, bar, (tile % a.tiles_c) * kTile, (a.tr0 + tile / a.tiles_c) * kTile);
-  };
-  if (threadIdx.x == 0) ring.fill(kNormSlots, load);
-  const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  TileEmit<1, false, POW2> emit(smem + NormColSmem::kEmit, a.out);
-  for (int i = 0; i < count; ++i) {
-    const int tile = tile_of(i);
-    const int tr = a.tr0 + tile / a.tiles_c, tc = tile % a.tiles_c;
-    const int64_t r0 = static_cast<int64_t>(tr) * kTile + rb * 8;
-    const int64_t c0 = static_cast<int64_t>(tc) * kTile + lane * 4;
-    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rs[8];
-    if (c0 < a.cols) load_gamma4(a.gamma, a.gamma_f32, c0, g);
+  const int tile = a.tiles_r * a.tiles_c - 1 - static_cast<int>(blockIdx.x);
+  const int tr = a.tr0 + tile / a.tiles_c, tc = tile % a.tiles_c;
+  const int64_t r0 = static_cast<int64_t>(tr) * kTile + rb * 8;
+  const int64_t c0 = static_cast<int64_t>(tc) * kNormColTile + cb * 4;
+  const bool cin = c0 < a.cols;
+  uint2 w[8];
+  float rs[8], g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int p = 0; p < 8; ++p) rs[p] = r0 + p < a.rows ? __ldg(a.rstd + r0 + p) : 0.0f;
-    float y[1][8][4];
-    const uint8_t* in = ring.next();
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      read4(in, p, y[0][p]);
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        fmul2(y[0][p][j], y[0][p][j + 1], y[0][p][j], y[0][p][j + 1], rs[p], rs[p]);
-        fmul2(y[0][p][j], y[0][p][j + 1], y[0][p][j], y[0][p][j + 1], g[j], g[j + 1]);
-      }
-    }
-    emit.step(y, tr, {tc}, [&] {
-      if (threadIdx.x == 0) ring.fill(1, load);
-    });
+  for (int p = 0; p < 8; ++p) {
+    const bool in = cin && r0 + p < a.rows;
+    w[p] = in ? *reinterpret_cast<const uint2*>(a.h + (r0 + p) * a.cols + c0) : make_uint2(0u, 0u);
+    rs[p] = in ? __ldg(a.rstd + r0 + p) : 0.0f;
   }
-  emit.finish();
-  if (threadIdx.x == 0) ring.drain();
+  if (cin) load_gamma4(a.gamma, a.gamma_f32, c0, g);
+  float y[8][4], m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    fmul2(y[p][0], y[p][1], bf16_lo(w[p].x), bf16_hi(w[p].x), rs[p], rs[p]);
+    fmul2(y[p][2], y[p][3], bf16_lo(w[p].y), bf16_hi(w[p].y), rs[p], rs[p]);
+    fmul2(y[p][0], y[p][1], y[p][0], y[p][1], g[0], g[1]);
+    fmul2(y[p][2], y[p][3], y[p][2], y[p][3], g[2], g[3]);
+    if (p & 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = max3_abs(m[j], y[p - 1][j], y[p][j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+  if (lane < 16) *reinterpret_cast<float4*>(&red[warp][cb * 4]) = make_float4(m[0], m[1], m[2], m[3]);
+  __syncthreads();
+  if (t < kNormColTile) {
+    float am = red[0][t];
+#pragma unroll
+    for (int i = 1; i < kNormColThreads / 32; ++i) am = fmaxf(am, red[i][t]);
+    float qs, s;
+    scale_near<POW2>(am, qs, s);
+    colq[t] = qs;
+    const int64_t c = static_cast<int64_t>(tc) * kNormColTile + t;
+    if (c < a.cols) a.s_t[static_cast<int64_t>(tr) * a.cols + c] = s;
+  }
+  __syncthreads();
+  const float4 k = *reinterpret_cast<const float4*>(&colq[cb * 4]);
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    fmul2(y[p][0], y[p][1], y[p][0], y[p][1], k.x, k.y);
+    fmul2(y[p][2], y[p][3], y[p][2], y[p][3], k.z, k.w);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint2*>(T + emit_t_offset(cb * 4 + j, rb)) =
+        make_uint2(e4m3x4(y[0][j], y[1][j], y[2][j], y[3][j]),
+                   e4m3x4(y[4][j], y[5][j], y[6][j], y[7][j]));
+  __syncthreads();
+  // tile column kk is 128 contiguous tokens of row tc*64 + kk of q_t
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int kk = i * 32 + (t >> 3), ch = t & 7;
+    const int64_t c = static_cast<int64_t>(tc) * kNormColTile + kk;
+    const int64_t tok = static_cast<int64_t>(tr) * kTile + ch * 16;
+    const uint2 lo = *reinterpret_cast<const uint2*>(T + emit_t_offset(kk, 2 * ch));
+    const uint2 hi = *reinterpret_cast<const uint2*>(T + emit_t_offset(kk, 2 * ch + 1));
+    if (c < a.cols && tok < a.rows_pad)
+      *reinterpret_cast<uint4*>(a.q_t + c * a.rows_pad + tok) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
 }
 
 // ---------------------------------------------------------------- backward
