@@ -170,7 +170,7 @@ template <int V, bool POW2>
 int launch_norm_rows(NormArgs a, cudaStream_t stream) {
   a.tpr = threads_per_row(a.cols / 8, V);
   const int groups = std::max(1, 256 / a.tpr);
-  const int64_t blocks = cdiv(a.row_end - a.row0, groups);
+  const int64_t blocks = cdiv(a.rows_pad, groups);
   const auto kernel = a.cols == 8 * static_cast<int64_t>(V) * a.tpr
                           ? rmsnorm_row_kernel<V, true, POW2>
                           : rmsnorm_row_kernel<V, false, POW2>;
@@ -186,15 +186,12 @@ int norm_rows(const NormArgs& a, const Device& dev, cudaStream_t stream) {
   // Measured at 16384 x 2048 with 1, 2, 4, 8 chunks: 54, 50, 48, 61 us. Few
   // rows: the most threads per row, for latency (512 x 2048: 3.9 us with one
   // chunk, 5.0 with four).
-  const bool many = a.row_end - a.row0 > 4 * static_cast<int64_t>(dev.sm_count);
+  const bool many = a.rows_pad > 4 * static_cast<int64_t>(dev.sm_count);
   if (chunks <= (many ? 32 : 1024)) return launch_norm_rows<1, POW2>(a, stream);
   if (many && chunks <= 64) return launch_norm_rows<2, POW2>(a, stream);
   if (chunks <= 2048) return launch_norm_rows<4, POW2>(a, stream);
   return launch_norm_rows<8, POW2>(a, stream);
 }
-
-// Rows whose h stays in L2 until the column pass reads it (half of its 126 MB).
-constexpr int64_t kNormChunkBytes = int64_t(64) << 20;
 
 template <bool POW2>
 int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* gamma,
@@ -202,6 +199,8 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
                      float* rstd, uint16_t* y, uint8_t* q, float* s, uint8_t* q_t, float* s_t,
                      void* stream) {
   if (rows < 0 || rows > kMaxRows || !cols_ok(cols, kMaxNormCols)) return FP8BW_ERR_SHAPE;
+  if (q_t != nullptr && cdiv(rows, 128) * cdiv(cols, kNormColTile) > INT32_MAX)
+    return FP8BW_ERR_SHAPE;
   if (!(eps >= 0.0f)) return FP8BW_ERR_SHAPE;
   const int64_t rp = pad16(rows), n = rows * cols;
   if (n > 0 && ((q == nullptr) != (s == nullptr) || (q_t == nullptr) != (s_t == nullptr)))
@@ -239,35 +238,23 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
   a.y = y;
   a.q = q;
   a.s = s;
-  if (q_t == nullptr) {
-    a.row0 = 0;
-    a.row_end = rp;
-    return norm_rows<POW2>(a, dev, cs);
-  }
-  const int64_t chunk = std::max<int64_t>(128, kNormChunkBytes / (2 * cols) / 128 * 128);
-  for (int64_t r0 = 0; r0 < rp; r0 += chunk) {
-    a.row0 = r0;
-    a.row_end = std::min(rp, r0 + chunk);
-    st = norm_rows<POW2>(a, dev, cs);
-    if (st != FP8BW_OK) return st;
-    NormColArgs c{};
-    c.h = residual != nullptr ? h : x;
-    c.rstd = rstd;
-    c.gamma = gamma;
-    c.gamma_f32 = a.gamma_f32;
-    c.rows = rows;
-    c.rows_pad = rp;
-    c.cols = cols;
-    c.tr0 = static_cast<int>(r0 / 128);
-    c.tiles_r = static_cast<int>(cdiv(a.row_end - r0, 128));
-    c.tiles_c = static_cast<int>(cdiv(cols, kNormColTile));
-    c.q_t = q_t;
-    c.s_t = s_t;
-    st = launched(launch_kernel(norm_col_kernel<POW2>, dim3(c.tiles_r * c.tiles_c),
+  st = norm_rows<POW2>(a, dev, cs);
+  if (st != FP8BW_OK || q_t == nullptr) return st;
+  NormColArgs c{};
+  c.h = residual != nullptr ? h : x;
+  c.rstd = rstd;
+  c.gamma = gamma;
+  c.gamma_f32 = a.gamma_f32;
+  c.rows = rows;
+  c.rows_pad = rp;
+  c.cols = cols;
+  c.tiles_r = static_cast<int>(cdiv(rp, 128));
+  c.tiles_c = static_cast<int>(cdiv(cols, kNormColTile));
+  c.q_t = q_t;
+  c.s_t = s_t;
+  const int64_t tiles = static_cast<int64_t>(c.tiles_r) * c.tiles_c;
+  return launched(launch_kernel(norm_col_kernel<POW2>, dim3(static_cast<unsigned>(tiles)),
                                 dim3(kNormColThreads), 0, cs, c));
-    if (st != FP8BW_OK) return st;
-  }
-  return FP8BW_OK;
 }
 
 // ---------------------------------------------------------------- norm, backward

@@ -69,16 +69,11 @@ __device__ __forceinline__ void load_gamma8(const void* gamma, int is_f32, int64
   }
 }
 
-// The same for four columns.
-__device__ __forceinline__ void load_gamma4(const void* gamma, int is_f32, int64_t c,
-                                            float (&g)[4]) {
-  if (is_f32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(gamma) + c));
-    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-  } else {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(gamma) + c));
-    g[0] = bf16_lo(w.x), g[1] = bf16_hi(w.x), g[2] = bf16_lo(w.y), g[3] = bf16_hi(w.y);
-  }
+// One of them.
+__device__ __forceinline__ float load_gamma(const void* gamma, int is_f32, int64_t c) {
+  return is_f32 ? __ldg(static_cast<const float*>(gamma) + c)
+                : __uint_as_float(static_cast<uint32_t>(
+                      __ldg(static_cast<const unsigned short*>(gamma) + c)) << 16);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -93,7 +88,6 @@ struct NormArgs {
   const uint16_t* residual;   // may be null: h = x
   const void* gamma;
   int gamma_f32;
-  int64_t row0, row_end;      // this launch's rows of [0, rows_pad)
   int64_t rows, rows_pad, cols;
   float eps;
   uint16_t* h;                // written when there is a residual
@@ -132,8 +126,8 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
   const int t = threadIdx.x - grp * tpr;
   const int groups = blockDim.x / tpr;
   const int lane = threadIdx.x & 31;
-  const int64_t row = a.row0 + static_cast<int64_t>(blockIdx.x) * groups + grp;
-  const bool live = row < a.rows && row < a.row_end;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * groups + grp;
+  const bool live = row < a.rows;
   const int chunks = static_cast<int>(a.cols >> 3);
   const int64_t base = row * a.cols;
   auto has = [&](int v) { return FULL || t + v * tpr < chunks; };
@@ -219,7 +213,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
   float qs, s;
   scale_near<POW2>(m[0] * rstd, qs, s);
   const float f = qs * rstd;
-  const bool out = row < a.row_end;
+  const bool out = row < a.rows_pad;
   const int64_t first = (t & ~15) + mine * tpr;       // first chunk of this lane's group
   if ((lane & (kShare - 1)) == 0 && out && (FULL || first < chunks))
     a.s[(first >> 4) * a.rows_pad + row] = s;
@@ -238,14 +232,14 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
 // 256 holds rows 8 * (t / 16) .. +7 and columns 4 * (t % 16) .. +3. A block does one
 // tile and four blocks share an SM: a tile is a chain of loads and barriers, and
 // the other blocks work meanwhile. (As steps of one 512-thread block per SM over
-// 128 x 128 tiles with a TMA ring: 63 us for both passes at 16384 x 2048.)
+// 128 x 128 tiles with a TMA ring 63 us for both passes at 16384 x 2048 instead of
+// 61; as persistent blocks that copy the next tile ahead 66.)
 struct NormColArgs {
   const uint16_t* h;
   const float* rstd;
   const void* gamma;
   int gamma_f32;
   int64_t rows, rows_pad, cols;
-  int tr0;                    // first row tile of this launch
   int tiles_r, tiles_c;
   uint8_t* q_t;
   float* s_t;
@@ -264,26 +258,34 @@ __global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const Norm
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rb = t >> 4, cb = t & 15;
   // last rows first: they are the most recently written, and still in L2
   const int tile = a.tiles_r * a.tiles_c - 1 - static_cast<int>(blockIdx.x);
-  const int tr = a.tr0 + tile / a.tiles_c, tc = tile % a.tiles_c;
+  const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
   const int64_t r0 = static_cast<int64_t>(tr) * kTile + rb * 8;
   const int64_t c0 = static_cast<int64_t>(tc) * kNormColTile + cb * 4;
-  const bool cin = c0 < a.cols;
+  // h * rstd; the norm weight joins a column's scale
   uint2 w[8];
-  float rs[8], g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float rs[8];
+  const uint16_t* h = a.h + r0 * a.cols + c0;
+  if (static_cast<int64_t>(tr + 1) * kTile <= a.rows &&
+      static_cast<int64_t>(tc + 1) * kNormColTile <= a.cols) {
+    const float4 ra = __ldg(reinterpret_cast<const float4*>(a.rstd + r0));
+    const float4 rc = __ldg(reinterpret_cast<const float4*>(a.rstd + r0) + 1);
+    rs[0] = ra.x, rs[1] = ra.y, rs[2] = ra.z, rs[3] = ra.w;
+    rs[4] = rc.x, rs[5] = rc.y, rs[6] = rc.z, rs[7] = rc.w;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const bool in = cin && r0 + p < a.rows;
-    w[p] = in ? *reinterpret_cast<const uint2*>(a.h + (r0 + p) * a.cols + c0) : make_uint2(0u, 0u);
-    rs[p] = in ? __ldg(a.rstd + r0 + p) : 0.0f;
+    for (int p = 0; p < 8; ++p, h += a.cols) w[p] = *reinterpret_cast<const uint2*>(h);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p, h += a.cols) {
+      const bool in = c0 < a.cols && r0 + p < a.rows;
+      w[p] = in ? *reinterpret_cast<const uint2*>(h) : make_uint2(0u, 0u);
+      rs[p] = in ? __ldg(a.rstd + r0 + p) : 0.0f;
+    }
   }
-  if (cin) load_gamma4(a.gamma, a.gamma_f32, c0, g);
   float y[8][4], m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     fmul2(y[p][0], y[p][1], bf16_lo(w[p].x), bf16_hi(w[p].x), rs[p], rs[p]);
     fmul2(y[p][2], y[p][3], bf16_lo(w[p].y), bf16_hi(w[p].y), rs[p], rs[p]);
-    fmul2(y[p][0], y[p][1], y[p][0], y[p][1], g[0], g[1]);
-    fmul2(y[p][2], y[p][3], y[p][2], y[p][3], g[2], g[3]);
     if (p & 1) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) m[j] = max3_abs(m[j], y[p - 1][j], y[p][j]);
@@ -294,13 +296,14 @@ __global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const Norm
   if (lane < 16) *reinterpret_cast<float4*>(&red[warp][cb * 4]) = make_float4(m[0], m[1], m[2], m[3]);
   __syncthreads();
   if (t < kNormColTile) {
+    const int64_t c = static_cast<int64_t>(tc) * kNormColTile + t;
+    const float g = c < a.cols ? load_gamma(a.gamma, a.gamma_f32, c) : 0.0f;
     float am = red[0][t];
 #pragma unroll
     for (int i = 1; i < kNormColThreads / 32; ++i) am = fmaxf(am, red[i][t]);
     float qs, s;
-    scale_near<POW2>(am, qs, s);
-    colq[t] = qs;
-    const int64_t c = static_cast<int64_t>(tc) * kNormColTile + t;
+    scale_near<POW2>(am * fabsf(g), qs, s);
+    colq[t] = qs * g;
     if (c < a.cols) a.s_t[static_cast<int64_t>(tr) * a.cols + c] = s;
   }
   __syncthreads();
