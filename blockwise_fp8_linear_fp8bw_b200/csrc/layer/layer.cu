@@ -127,29 +127,22 @@ int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   return FP8BW_OK;
 }
 
-int encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
-              uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-              CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode;
-  const int st = tensor_map_encoder(&encode);
-  if (st != FP8BW_OK) return st;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1u, 1u};
-  return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? FP8BW_OK
-             : FP8BW_ERR_CUDA;
-}
-
 // bf16 [rows, cols] with rows of row_bytes, read in 128 x 128 tiles.
 int encode_tiles(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                  int64_t row_bytes) {
-  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, static_cast<uint64_t>(cols),
-                   static_cast<uint64_t>(rows), static_cast<uint64_t>(row_bytes), kTile, kTile,
-                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  const int st = tensor_map_encoder(&encode);
+  if (st != FP8BW_OK) return st;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {kTile, kTile};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FP8BW_OK
+             : FP8BW_ERR_CUDA;
 }
 
 template <typename K>
@@ -522,12 +515,6 @@ int encode_operand(CUtensorMap* map, const NsOperand& o, int rows) {
              : FP8BW_ERR_CUDA;
 }
 
-int encode_boxes(CUtensorMap* map, const void* p, int64_t rows, int64_t cols) {
-  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, p, static_cast<uint64_t>(cols),
-                   static_cast<uint64_t>(rows), static_cast<uint64_t>(2 * cols), 32, 32,
-                   CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
-}
-
 template <int BN>
 int ns_clusters(const Device& dev, int* clusters) {
   static DevicePrep prep;
@@ -586,15 +573,14 @@ int ns_launch(NsGemm* g, int count, const Device& dev, cudaStream_t stream) {
     j.bf16 = g[i].bf16;
     j.c = g[i].c;
     j.c2 = g[i].c2;
+    j.out = g[i].out;
+    j.lo = g[i].lo;
     j.alpha = g[i].alpha;
     j.beta = g[i].beta;
     j.beta2 = g[i].beta2;
     j.diag = g[i].diag;
     st = encode_operand(&maps.a[i], g[i].a, ns::BM);
     if (st == FP8BW_OK) st = encode_operand(&maps.b[i], g[i].b, bn / 2);
-    if (st == FP8BW_OK && g[i].lo != nullptr)
-      st = encode_boxes(&maps.lo[i], g[i].lo, g[i].rows, g[i].cols);
-    if (st == FP8BW_OK) st = encode_boxes(&maps.out[i], g[i].out, g[i].rows, g[i].cols);
     if (st != FP8BW_OK) return st;
   }
   args.count = count;
