@@ -19,6 +19,7 @@ The norm's and the gated product's outputs are rounded once, to E4M3. Any number
 of tokens works: rows are padded to a multiple of 16 with zero codes.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -58,6 +59,7 @@ class BlockwiseFp8MLPFunction(torch.autograd.Function):
         return (y, n.h) if ctx.has_residual else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         (h, rstd, gamma, qx_t, sx_t, gu, qa_t, sa_t, qw1_t, sw1, qw2_t,
          sw2) = ctx.saved_tensors
@@ -109,7 +111,12 @@ class BlockwiseFp8MLP(torch.nn.Module):
     gradient as in BlockwiseFp8Linear.
 
     Without gradients only the row-wise codes are computed; `freeze()` then keeps
-    the weights' codes for the calls that follow (until `unfreeze()`)."""
+    the weights' codes for the calls that follow (until `unfreeze()`).
+
+    A training step can be captured into a CUDA graph. Warm up on the stream that
+    will capture, and let go of what eager steps returned before capturing: an
+    eager graph that still holds the leaves has autograd synchronise with its
+    stream, which a capture does not allow."""
 
     def __init__(self, hidden, ffn, eps=1e-6, device=None, pow2=False):
         super().__init__()

@@ -28,15 +28,31 @@ class MuonH(torch.optim.Optimizer):
             raise ValueError("lr must be >= 0 and momentum in [0, 1)")
         super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov, steps=steps,
                                       coeffs=tuple(coeffs), eps=eps, project=project))
-        for group in self.param_groups:
-            for p in group["params"]:
-                if p.dim() != 2 or p.shape[0] % 16 or p.shape[1] % 16:
-                    raise ValueError("MuonH takes 2-D weights with sides that are multiples of "
-                                     "16, got %s" % (tuple(p.shape),))
+
+    def add_param_group(self, group):
+        super().add_param_group(group)
+        for p in self.param_groups[-1]["params"]:
+            if p.dim() != 2 or p.shape[0] % 16 or p.shape[1] % 16:
+                del self.param_groups[-1]
+                raise ValueError("MuonH takes 2-D weights with sides that are multiples of "
+                                 "16, got %s" % (tuple(p.shape),))
+
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        # the base class rounds a weight's state to the weight's type; it stays fp32
+        saved = [i for group in state_dict["param_groups"] for i in group["params"]]
+        params = [p for group in self.param_groups for p in group["params"]]
+        for i, p in zip(saved, params):
+            for key, value in state_dict["state"].get(i, {}).items():
+                self.state[p][key] = value.detach().to(
+                    device=p.device, dtype=torch.float32, copy=True)
 
     def _state_of(self, p, group):
         state = self.state[p]
         if not state:
+            if torch.cuda.is_current_stream_capturing():
+                # a replay would start from the captured state every time
+                raise RuntimeError("MuonH: take one step before capturing one in a graph")
             w = p.detach().float()
             state["momentum"] = torch.zeros_like(w)
             state["radius"] = torch.linalg.vector_norm(w)

@@ -216,7 +216,7 @@ def test_step_in_a_graph():
 
     def step():
         y, h = m(x, r)
-        return y, *torch.autograd.grad([y, h], [x, m.gamma], [dy, dh])
+        return y.detach(), *torch.autograd.grad([y, h], [x, m.gamma], [dy, dh])
 
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -242,3 +242,77 @@ def test_step_in_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert all(torch.equal(a, w.main_grad) for a, w in zip(mains, (m.w_gate_up, m.w_down)))
     del g
+
+
+@pytest.mark.parametrize("residual", [True, False])
+def test_no_tokens(residual):
+    """A block over an empty batch: empty results, zero gradients."""
+    torch, _, mlp, _ = _mods()
+    m = _block(torch, mlp)
+    x, r, dy, _ = (t[:0] for t in _inputs(torch, 1, 272, 41))
+    x.requires_grad_()
+    y, h = m(x, r if residual else None)
+    y.backward(dy)
+    assert y.shape == h.shape == x.grad.shape == (0, 272)
+    assert all(not p.grad.any() for p in m.parameters())
+    with torch.no_grad():
+        assert m(x)[0].shape == (0, 272)
+
+
+def test_second_derivatives_are_refused():
+    torch, _, mlp, _ = _mods()
+    m = _block(torch, mlp)
+    x, _, dy, _ = _inputs(torch, 16, 272, 42)
+    x.requires_grad_()
+    y, _ = m(x)
+    dx, = torch.autograd.grad(y, x, dy.requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.float().sum().backward()
+
+
+def test_optimiser_refuses_to_capture_its_first_step():
+    """Its state would be set up anew in every replay. A later step replays as it
+    runs eagerly."""
+    torch, _, _, muon = _mods()
+    torch.manual_seed(5)
+    start = torch.randn(64, 96, device="cuda")
+    grads = [torch.randn(64, 96, device="cuda") for _ in range(3)]
+    w, v = (torch.nn.Parameter(start.clone()) for _ in range(2))
+    w.grad, v.grad = grads[0].clone(), grads[0].clone()
+    opt, eager = muon.MuonH([w], lr=0.1), muon.MuonH([v], lr=0.1)
+    with pytest.raises(RuntimeError, match="one step before"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            opt.step()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        opt.step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        opt.step()
+    for grad in grads:
+        v.grad.copy_(grad)
+        eager.step()
+    for grad in grads[1:]:
+        w.grad.copy_(grad)
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(w, v)
+    del g
+
+
+def test_running_out_of_memory_raises_torchs_error():
+    torch, ops, _, _ = _mods()
+    gu = torch.zeros(1 << 14, 1 << 13, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.empty_cache()
+    used = torch.cuda.memory_reserved()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((used + (16 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            ops.swiglu_quantize(gu)        # 64 MB of codes
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert not ops.swiglu_quantize(gu).q.any()

@@ -157,3 +157,41 @@ def test_binding_refuses_before_the_library():
         ops.rmsnorm_backward(bf, bf, torch.ones(3), torch.ones(64))
     with pytest.raises(ValueError, match="CUDA"):
         ops.newton_schulz(torch.zeros(32, 32))
+
+
+def test_optimiser_state_stays_fp32_and_groups_are_checked():
+    """Loading a checkpoint does not round the fp32 state to a bf16 weight's type;
+    groups added later are checked as the first ones are."""
+    from blockwise_fp8_linear_fp8bw_b200.muon import MuonH
+    g = torch.Generator().manual_seed(3)
+    p = [torch.nn.Parameter(torch.randn(16, 32, generator=g).bfloat16()) for _ in range(2)]
+    opt = MuonH(p)
+    for w in p:
+        opt.state[w] = {"momentum": torch.randn(16, 32, generator=g),
+                        "radius": torch.randn((), generator=g),
+                        "master": torch.randn(16, 32, generator=g)}
+    saved = opt.state_dict()
+    q = [torch.nn.Parameter(w.detach().clone()) for w in p]
+    new = MuonH(q)
+    new.load_state_dict(saved)
+    for w, v in zip(p, q):
+        for key, t in opt.state[w].items():
+            assert new.state[v][key].dtype == torch.float32
+            assert torch.equal(new.state[v][key], t)
+            assert new.state[v][key].data_ptr() != t.data_ptr()
+    for shape in ((16,), (24, 32), (16, 8)):
+        with pytest.raises(ValueError, match="multiples of"):
+            new.add_param_group({"params": [torch.nn.Parameter(torch.zeros(shape))]})
+    assert len(new.param_groups) == 1
+
+
+def test_binding_passes_errors_of_its_arguments_on():
+    class Neither:
+        def __bool__(self):
+            raise LookupError("neither")
+
+    gu = torch.zeros(16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.swiglu_quantize(gu, colwise=Neither())     # the tensor is refused first
+    with pytest.raises(TypeError):
+        ops.newton_schulz(torch.zeros(16, 16), steps="5")
