@@ -16,7 +16,8 @@
 // row sum is a warp shuffle plus, when several warps share a row, one step
 // through shared memory. 16 consecutive threads hold one 1x128 group.
 // Column-wise codes need all 128 rows' rstd first: norm_col_kernel makes a
-// second pass over h in 128x128 tiles, last rows first, while h is still in L2.
+// second pass over h in 128 x 64 tiles, last rows first, while the end of h is
+// still in L2.
 #pragma once
 
 #include "../common.cuh"
@@ -30,13 +31,22 @@ __device__ __forceinline__ uint4 ld16(const void* p) {
   return *reinterpret_cast<const uint4*>(p);
 }
 
+// Inputs may come from the kernel before this one, so no load may move above
+// grid_dependency_wait(): they are volatile (that keeps their order with the
+// wait), not loads of constant memory.
+
 // Read once, not needed again: keep it from displacing what is re-read from L2.
 __device__ __forceinline__ uint4 ld16_stream(const void* p) {
-  return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint4 v;
+  asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
-// A second read that the compiler must not merge with the first (whose
-// registers would then have to live until here).
+// A load of its own: the compiler neither merges it with another of the same
+// address (whose registers would then have to live until here) nor holds it back
+// behind a store.
 __device__ __forceinline__ uint4 ld16_again(const void* p) {
   uint4 v;
   asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -60,20 +70,22 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
 __device__ __forceinline__ void load_gamma8(const void* gamma, int is_f32, int64_t c,
                                             float (&g)[8]) {
   if (is_f32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(gamma) + c);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-    g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+    const float* p = static_cast<const float*>(gamma) + c;
+    const uint4 a = ld16_again(p), b = ld16_again(p + 4);
+    g[0] = __uint_as_float(a.x), g[1] = __uint_as_float(a.y);
+    g[2] = __uint_as_float(a.z), g[3] = __uint_as_float(a.w);
+    g[4] = __uint_as_float(b.x), g[5] = __uint_as_float(b.y);
+    g[6] = __uint_as_float(b.z), g[7] = __uint_as_float(b.w);
   } else {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gamma) + c)), g);
+    unpack8(ld16_again(static_cast<const uint16_t*>(gamma) + c), g);
   }
 }
 
 // One of them.
 __device__ __forceinline__ float load_gamma(const void* gamma, int is_f32, int64_t c) {
-  return is_f32 ? __ldg(static_cast<const float*>(gamma) + c)
-                : __uint_as_float(static_cast<uint32_t>(
-                      __ldg(static_cast<const unsigned short*>(gamma) + c)) << 16);
+  return is_f32 ? static_cast<const float*>(gamma)[c]
+                : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(gamma)[c])
+                                  << 16);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -267,8 +279,8 @@ __global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const Norm
   const uint16_t* h = a.h + r0 * a.cols + c0;
   if (static_cast<int64_t>(tr + 1) * kTile <= a.rows &&
       static_cast<int64_t>(tc + 1) * kNormColTile <= a.cols) {
-    const float4 ra = __ldg(reinterpret_cast<const float4*>(a.rstd + r0));
-    const float4 rc = __ldg(reinterpret_cast<const float4*>(a.rstd + r0) + 1);
+    const float4 ra = reinterpret_cast<const float4*>(a.rstd + r0)[0];
+    const float4 rc = reinterpret_cast<const float4*>(a.rstd + r0)[1];
     rs[0] = ra.x, rs[1] = ra.y, rs[2] = ra.z, rs[3] = ra.w;
     rs[4] = rc.x, rs[5] = rc.y, rs[6] = rc.z, rs[7] = rc.w;
 #pragma unroll
@@ -278,7 +290,7 @@ __global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const Norm
     for (int p = 0; p < 8; ++p, h += a.cols) {
       const bool in = c0 < a.cols && r0 + p < a.rows;
       w[p] = in ? *reinterpret_cast<const uint2*>(h) : make_uint2(0u, 0u);
-      rs[p] = in ? __ldg(a.rstd + r0 + p) : 0.0f;
+      rs[p] = in ? a.rstd[r0 + p] : 0.0f;
     }
   }
   float y[8][4], m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -402,7 +414,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
     for (int r = 0; r < R; ++r) {
       const int64_t row = b + r * groups + grp;
       const bool live = row < a.rows;
-      rs[r] = live ? __ldg(a.rstd + row) : 0.0f;
+      rs[r] = live ? a.rstd[row] : 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int64_t at = row * a.cols + col(v);

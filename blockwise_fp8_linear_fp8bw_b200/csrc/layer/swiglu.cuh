@@ -32,12 +32,13 @@ __device__ __forceinline__ void sigmoid2(float x0, float x1, float& s0, float& s
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(e1));
 }
 
-// y = gate * up * sigmoid(gate), two elements.
+// y = gate * sigmoid(gate) * up, two elements (in this order nothing overflows
+// that the result does not).
 __device__ __forceinline__ void glu2(const float* g, const float* u, float* y) {
   float s0, s1, w0, w1;
   sigmoid2(g[0], g[1], s0, s1);
-  fmul2(w0, w1, u[0], u[1], g[0], g[1]);
-  fmul2(y[0], y[1], w0, w1, s0, s1);
+  fmul2(w0, w1, g[0], g[1], s0, s1);
+  fmul2(y[0], y[1], w0, w1, u[0], u[1]);
 }
 
 // ---------------------------------------------------------------- row-wise only

@@ -71,9 +71,10 @@ __device__ __forceinline__ void scale_near(float amax, float& qscale, float& s) 
   if constexpr (POW2) {
     group_scale_pow2(amax, qscale, s);
   } else {
+    // (of amax / 16, so that no finite amax has a subnormal reciprocal)
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax));
-    r *= 448.0f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * 0.0625f));
+    r *= 28.0f;
     const bool none = !isfinite(r) || amax == 0.0f;
     qscale = none ? 1.0f : r;
     s = none ? 1.0f : amax * (1.0f / 448.0f);

@@ -174,6 +174,37 @@ def test_zero_rows_and_large_gates():
     assert not bool(torch.isnan(d.q.view(torch.float8_e4m3fn).float()).any())
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+def test_values_near_the_end_of_fp32s_range(pow2):
+    """Maxima between 2^126 and 2^128 (a reciprocal below the normal numbers), and
+    products that leave the range before the sigmoid is applied."""
+    torch, ops = _t(), _ops()
+    gate = (_normal((48, 256), 170).float().abs() * 10 + 20).clamp(max=60)
+    up = _normal((48, 256), 171).float().clamp(-3, 3) * 2.0 ** 120
+    gate[:, ::17] = -100.0
+    up[:, ::17] = 2.0 ** 126
+    gu = torch.cat([gate, up], 1).bfloat16()
+    a, err = R.glu(gu)
+    assert 2.0 ** 126 < float(a.abs().max()) < 2.0 ** 128
+    out = ops.swiglu_quantize(gu, colwise=True, pow2=pow2)
+    R.check_codes(out.q, out.s, a, err, 1, pow2, 48)
+    R.check_codes(out.q_t, out.s_t, a, err, 0, pow2, 48)
+    gu[:, 256:] = _normal((48, 256), 172).clamp(-3, 3)
+    da = up.bfloat16()
+    d, err = R.glu_backward(da, gu)
+    assert 2.0 ** 126 < float(d.abs().max()) < 2.0 ** 128
+    out = ops.swiglu_backward_quantize(da, gu, pow2=pow2)
+    R.check_codes(out.q, out.s, d, err, 1, pow2, 48)
+    R.check_codes(out.q_t, out.s_t, d, err, 0, pow2, 48)
+    x = _normal((48, 256), 173).clamp(-3, 3)
+    gamma = torch.full((256,), 2.0 ** 125, device="cuda")
+    _, _, v, err = R.norm(x, None, gamma, 1e-6)
+    assert 2.0 ** 126 < float(v.abs().max()) < 2.0 ** 128
+    n = ops.rmsnorm_quantize(x, gamma, None, 1e-6, colwise=True, pow2=pow2)
+    R.check_codes(n.q, n.s, v, err, 1, pow2, 48)
+    R.check_codes(n.q_t, n.s_t, v, err, 0, pow2, 48)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_non_finite_values_stay_in_their_row(bad):
     torch, ops = _t(), _ops()
