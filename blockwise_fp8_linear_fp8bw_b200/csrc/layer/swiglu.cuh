@@ -226,10 +226,154 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) ring.drain();
 }
 
-// Backward for f no multiple of 128: the 1x128 groups of d then straddle the
-// dgate/dup boundary, so each tile of d's 2f columns is computed by itself,
-// every 4-column run from its own gate, up and da columns (read twice in all,
-// with plain loads).
+// Backward for f = 128 m + r, r > 0: the dup half of d then starts in the middle
+// of a tile, so input tile s (columns 128 s ..) gives dgate's tile s, but dup
+// values for two tiles of d: its first 128 - r columns end tile m + s, its last r
+// begin tile m + s + 1. The lanes' columns of the dup tile are their input columns
+// turned by r; one of the two parts waits in shared memory (fp32, for the thread
+// that wrote it) for the block's next step, whose other part completes it. A block
+// takes consecutive tiles of a row of tiles, upwards for r <= 64 (the last r
+// columns are kept) and downwards beyond (the first 128 - r), so that half a tile
+// is enough. Two pieces come from plain loads: what the block's first step would
+// have been left by the one before it, and in tile m the first dup columns, which
+// share it with the end of dgate.
+// (16384 x 6128: 209 us; 214 with one run per block, for then the blocks are all
+// over the tensor; 217 with the values shuffled into place instead of other columns
+// per lane; 217 with the pieces of a run's start copied ahead, for the registers;
+// 338 with the kernel below.)
+constexpr int kGluShiftSlots = 5;
+constexpr int kGluRun = 16;
+using GluShiftRing = TileRing<3, kGluShiftSlots>;
+struct GluShiftSmem {
+  static constexpr int kEmit = (GluShiftRing::kBytes + 127) / 128 * 128;
+  static constexpr int kKept = kEmit + TileEmit<2, true, false>::kBytes;   // half a tile
+  static constexpr int kAlloc = kKept + kTile * kTile * 2 + 128;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
+struct GluShiftArgs {
+  const uint16_t* gu;
+  const uint16_t* da;
+  int64_t rows;
+  int f, tiles_r;
+  CodesOut out;
+};
+
+template <bool POW2>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    swiglu_bwd_shift_kernel(const __grid_constant__ CUtensorMap map_g,
+                            const __grid_constant__ CUtensorMap map_u,
+                            const __grid_constant__ CUtensorMap map_da, const GluShiftArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align128(smem_raw);
+  const int m = a.f / kTile, r = a.f % kTile, per_row = m + 1;
+  const bool down = r > kTile / 2;
+  const int64_t total = static_cast<int64_t>(a.tiles_r) * per_row;
+  // tiles in runs of kGluRun by all blocks in turn; what is left, in shorter ones
+  const int full = static_cast<int>(total / (kGluRun * gridDim.x));
+  const int64_t done = static_cast<int64_t>(full) * kGluRun * gridDim.x;
+  const int last = static_cast<int>(done + (total - done) * blockIdx.x / gridDim.x);
+  const int count =
+      full * kGluRun + static_cast<int>(done + (total - done) * (blockIdx.x + 1) / gridDim.x) - last;
+  auto tile_at = [&](int i) {
+    const int k = i / kGluRun;
+    return k < full ? static_cast<int>(k * gridDim.x + blockIdx.x) * kGluRun + i % kGluRun
+                    : last + i - full * kGluRun;
+  };
+  GluShiftRing ring(smem, count);
+  if (threadIdx.x == 0) {
+    ring.init();
+    prefetch_tmap(&map_g);
+    prefetch_tmap(&map_u);
+    prefetch_tmap(&map_da);
+  }
+  TileEmit<2, true, POW2>::init(smem + GluShiftSmem::kEmit);
+  __syncthreads();
+  launch_dependents();
+  grid_dependency_wait();
+  auto input_tile = [&](int t) { return down ? m - t % per_row : t % per_row; };
+  auto load = [&](int i, int n, uint32_t dst, uint32_t bar) {
+    const int t = tile_at(i);
+    tma_load_2d(dst, n == 0 ? &map_g : n == 1 ? &map_u : &map_da, bar, input_tile(t) * kTile,
+                t / per_row * kTile);
+  };
+  if (threadIdx.x == 0) ring.fill(kGluShiftSlots, load);
+  TileEmit<2, true, POW2, true> emit(smem + GluShiftSmem::kEmit, a.out);
+
+  const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31, rot = r / 4;
+  emit.turn = rot;
+  const int dl = emit.lane_of(1);          // columns 4 dl .. of the dup tile
+  const bool keeps = down ? dl >= rot : dl < rot;
+  float4* kept = reinterpret_cast<float4*>(smem + GluShiftSmem::kKept) + rb * 8 * 16 +
+                 (down ? dl - rot : dl);                       // of row p: at 16 p
+  // dup of this thread's 8 rows of row tile tr, four columns from c on (0 outside):
+  // all loads first, then `put(p, values)`
+  auto dup_at = [&](int tr, int c, auto&& put) {
+    const int64_t row = static_cast<int64_t>(tr) * kTile + rb * 8;
+    uint2 wg[8], wd[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const bool in = row + p < a.rows && c >= 0 && c < a.f;
+      wg[p] = wd[p] = make_uint2(0u, 0u);
+      if (in) wg[p] = *reinterpret_cast<const uint2*>(a.gu + (row + p) * 2 * a.f + c);
+      if (in) wd[p] = *reinterpret_cast<const uint2*>(a.da + (row + p) * a.f + c);
+    }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float g[4] = {bf16_lo(wg[p].x), bf16_hi(wg[p].x), bf16_lo(wg[p].y), bf16_hi(wg[p].y)};
+      const float d[4] = {bf16_lo(wd[p].x), bf16_hi(wd[p].x), bf16_lo(wd[p].y), bf16_hi(wd[p].y)};
+      float v[4], unused[2];
+      glu_grad2(g, g, d, unused, v);
+      glu_grad2(g + 2, g + 2, d + 2, unused, v + 2);
+      put(p, v);
+    }
+  };
+  for (int i = 0; i < count; ++i) {
+    const int t = tile_at(i), tr = t / per_row, s = input_tile(t);
+    if (i % kGluRun == 0 && keeps) {       // a run starts
+      dup_at(tr, (down ? s + 1 : s) * kTile - r + dl * 4, [&](int p, const float(&v)[4]) {
+        kept[16 * p] = make_float4(v[0], v[1], v[2], v[3]);
+      });
+    }
+    float y[2][8][4];
+    const uint8_t* gate = ring.next();
+    const uint8_t* up = ring.next();
+    const uint8_t* da = ring.next();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float g[4], u[4], d[4];
+      read4(gate, p, g);
+      read4(up, p, u);
+      read4(da, p, d);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) glu_grad2(g + j, u + j, d + j, &y[0][p][j], &y[1][p][j]);
+      if (keeps) {
+        // (nothing lies right of tile m)
+        const float4 k = down && s == m ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : kept[16 * p];
+        kept[16 * p] = make_float4(y[1][p][0], y[1][p][1], y[1][p][2], y[1][p][3]);
+        y[1][p][0] = k.x, y[1][p][1] = k.y, y[1][p][2] = k.z, y[1][p][3] = k.w;
+      }
+    }
+    if (s == m && lane >= rot) {
+      dup_at(tr, lane * 4 - r, [&](int p, const float(&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[0][p][j] = v[j];
+      });
+    }
+    // upwards, the first step of a row only leaves its end behind: its other dup
+    // columns are those of tile m (a tile past the end is not written)
+    const int t1 = down ? m + s + 1 : s > 0 ? m + s : 2 * m + 2;
+    emit.step(y, tr, {s, t1}, [&] {
+      if (threadIdx.x == 0) ring.fill(3, load);
+    });
+  }
+  emit.finish();
+  if (threadIdx.x == 0) ring.drain();
+}
+
+// The same for few tiles: each tile of d's 2f columns by itself, every 4-column
+// run from its own gate, up and da columns (read twice in all, with plain loads),
+// in two blocks per SM. Half the work per block, and no second tile to wait for:
+// 777 x 1360 7.1 us against 8.7 above, 300 x 1360 6.2 and 8.8.
 struct GluRaggedArgs {
   const uint16_t* gu;
   const uint16_t* da;

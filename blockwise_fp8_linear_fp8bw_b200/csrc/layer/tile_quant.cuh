@@ -123,7 +123,8 @@ __device__ __forceinline__ int emit_t_offset(int k, int u) {
 // them, the transposed codes of a step leave shared memory during the next one:
 // between the barriers lie this step's row codes, the last step's transposed
 // codes and (in a few warps) the column scales.
-template <int NOUT, bool ROW, bool POW2>
+// With TURN, lane l holds columns 4 l' .. of the second tile, l' = (l + turn) % 32.
+template <int NOUT, bool ROW, bool POW2, bool TURN = false>
 struct TileEmit {
   static constexpr int kT = 0;                                   // NOUT x 16 KB
   // Column maxima, combined by shared-memory atomics on the bits (they are not
@@ -136,8 +137,14 @@ struct TileEmit {
 
   uint8_t* smem;
   const CodesOut& out;
-  int64_t row_at, col_at;      // this thread's offsets in a tile of q and q_t
+  int64_t row_at, col_at;      // offsets in a tile of q (its rows) and of q_t
   int last_tr = -1, last_tc[NOUT];
+  int turn = 0;
+
+  __device__ __forceinline__ int lane_of(int n) const {
+    const int lane = threadIdx.x & 31;
+    return TURN && n == 1 ? (lane + turn) & 31 : lane;
+  }
 
   // All threads, before the block's first barrier.
   __device__ __forceinline__ static void init(uint8_t* p) {
@@ -146,7 +153,7 @@ struct TileEmit {
 
   __device__ __forceinline__ TileEmit(uint8_t* p, const CodesOut& o) : smem(p), out(o) {
     const int t = threadIdx.x;
-    row_at = static_cast<int64_t>((t >> 5) * 8) * o.cols + (t & 31) * 4;
+    row_at = static_cast<int64_t>((t >> 5) * 8) * o.cols;
     col_at = static_cast<int64_t>(t >> 3) * o.rows + (t & 7) * 16;
   }
 
@@ -160,7 +167,7 @@ struct TileEmit {
   template <typename Freed>
   __device__ __forceinline__ void step(const float (&y)[NOUT][8][4], int tr,
                                        const int (&tc)[NOUT], Freed&& freed) {
-    const int t = threadIdx.x, rb = t >> 5, lane = t & 31;
+    const int t = threadIdx.x, rb = t >> 5;
     int* red = reinterpret_cast<int*>(smem + kRed);
     float* colq = reinterpret_cast<float*>(smem + kColQ);
     // column maxima of this warp's 8 rows
@@ -176,7 +183,7 @@ struct TileEmit {
       // column 4l + j at 32j + l: a warp's 32 addresses are in 32 banks
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        atomicMax(red + n * kTile + j * 32 + lane, __float_as_int(m[j]));
+        atomicMax(red + n * kTile + j * 32 + lane_of(n), __float_as_int(m[j]));
     }
     __syncthreads();
     freed();
@@ -195,12 +202,13 @@ struct TileEmit {
     if (last_tr >= 0) write_transposed();
     if constexpr (ROW) {
 #pragma unroll
-      for (int n = 0; n < NOUT; ++n) write_rows(y[n], tr, tc[n]);
+      for (int n = 0; n < NOUT; ++n) write_rows(y[n], tr, tc[n], lane_of(n));
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NOUT; ++n) {
       uint8_t* T = smem + kT + n * kTile * kTile;
+      const int lane = lane_of(n);
       const float4 k4 = *reinterpret_cast<const float4*>(colq + n * kTile + lane * 4);
       float v[8][4];
 #pragma unroll
@@ -245,7 +253,9 @@ struct TileEmit {
     }
   }
 
-  __device__ __forceinline__ void write_rows(const float (&y)[8][4], int tr, int tc) const {
+  // `col`: the lane whose columns this one holds
+  __device__ __forceinline__ void write_rows(const float (&y)[8][4], int tr, int tc,
+                                             int col) const {
     const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // row maxima; lane l computes the scale of row l & 7
     float mine = 0.0f;
@@ -260,8 +270,8 @@ struct TileEmit {
     const bool rin = rb * 8 < left(out.rows, tr) && left(out.cols, tc) > 0;
     const int64_t r0 = static_cast<int64_t>(tr) * kTile;
     if (lane < 8 && rin) out.s[static_cast<int64_t>(tc) * out.rows + r0 + rb * 8 + lane] = s;
-    uint8_t* q = out.q + r0 * out.cols + static_cast<int64_t>(tc) * kTile + row_at;
-    const bool in = rin && lane * 4 < left(out.cols, tc);
+    uint8_t* q = out.q + r0 * out.cols + static_cast<int64_t>(tc) * kTile + row_at + col * 4;
+    const bool in = rin && col * 4 < left(out.cols, tc);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const float k = __shfl_sync(0xFFFFFFFFu, qs, p);

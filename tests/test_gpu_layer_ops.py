@@ -106,6 +106,10 @@ def test_norm_backward_against_differences():
 
 GLU_SIZES = [(1, 16), (1, 6144), (7, 144), (16, 128), (17, 256), (128, 640),
              (129, 1360), (333, 272), (1000, 1024), (2050, 48)]
+# for the backward pass also widths whose end, over several rows of tiles per
+# block, is 16 to 112 columns past a multiple of 128
+GLU_BWD_SIZES = GLU_SIZES + [(6500, 464), (9000, 192), (4000, 720), (3000, 1296),
+                             (7000, 112), (2700, 880), (130, 80), (40, 2032)]
 
 
 @pytest.mark.parametrize("rows,f", GLU_SIZES)
@@ -123,7 +127,7 @@ def test_glu(rows, f, pow2):
     ops.fp8bw_check_device_error()
 
 
-@pytest.mark.parametrize("rows,f", GLU_SIZES)
+@pytest.mark.parametrize("rows,f", GLU_BWD_SIZES)
 @pytest.mark.parametrize("pow2", [False, True])
 def test_glu_backward(rows, f, pow2):
     ops = _ops()
