@@ -224,7 +224,13 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
   if (a.q == nullptr) return;
   float qs, s;
   scale_near<POW2>(m[0] * rstd, qs, s);
-  const float f = qs * rstd;
+  float f = qs * rstd;
+  if constexpr (!POW2) {
+    // rstd cancels: 448 / max|h gamma|, three roundings fewer (not where a scale of
+    // 1 stands for none, or something is not finite)
+    const float d = near_448_over(m[0]);
+    if (isfinite(d) && isfinite(rstd) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) f = d;
+  }
   const bool out = row < a.rows_pad;
   const int64_t first = (t & ~15) + mine * tpr;       // first chunk of this lane's group
   if ((lane & (kShare - 1)) == 0 && out && (FULL || first < chunks))

@@ -62,19 +62,27 @@ __device__ __forceinline__ float max3_abs(float m, float a, float b) {
   return r;
 }
 
-// scale_of for the fused kernels: the reciprocals are within 2 ulp instead of
+// 448 / amax within 2 ulp: the approximate reciprocal and one Newton step (of
+// amax / 16, so that no finite amax has a subnormal reciprocal). 0 for infinity,
+// infinite or NaN where the quotient is.
+__device__ __forceinline__ float near_448_over(float amax) {
+  const float a = amax * 0.0625f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  const float e = fmaf(-a, r, 1.0f);
+  return 28.0f * (fabsf(e) < 1.0f ? fmaf(r, e, r) : r);
+}
+
+// scale_of for the fused kernels: the quotients are within 2 ulp instead of
 // correctly rounded (two IEEE divisions cost some 40 instructions and their
-// latency, in every step). With amax / 448 to 1 ulp and 448 / amax to 2, amax still
-// encodes as 448, and other codes differ only for values within 2^-21 of a tie.
+// latency, in every step). amax still encodes as 448, and other codes differ only
+// for values within 2^-21 of a tie.
 template <bool POW2>
 __device__ __forceinline__ void scale_near(float amax, float& qscale, float& s) {
   if constexpr (POW2) {
     group_scale_pow2(amax, qscale, s);
   } else {
-    // (of amax / 16, so that no finite amax has a subnormal reciprocal)
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * 0.0625f));
-    r *= 28.0f;
+    const float r = near_448_over(amax);
     const bool none = !isfinite(r) || amax == 0.0f;
     qscale = none ? 1.0f : r;
     s = none ? 1.0f : amax * (1.0f / 448.0f);
