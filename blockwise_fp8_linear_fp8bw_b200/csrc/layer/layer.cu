@@ -174,14 +174,19 @@ int launch_norm_rows(NormArgs a, cudaStream_t stream) {
 template <bool POW2>
 int norm_rows(const NormArgs& a, const Device& dev, cudaStream_t stream) {
   const int64_t chunks = a.cols / 8;
-  // Many rows: four chunks per thread (64 registers: 32 warps per SM with up to
-  // eight 16-byte loads each in flight); two and one where a row has too few.
-  // Measured at 16384 x 2048 with 1, 2, 4, 8 chunks: 54, 50, 48, 61 us. Few
-  // rows: the most threads per row, for latency (512 x 2048: 3.9 us with one
-  // chunk, 5.0 with four).
-  const bool many = a.rows_pad > 4 * static_cast<int64_t>(dev.sm_count);
-  if (chunks <= (many ? 32 : 1024)) return launch_norm_rows<1, POW2>(a, stream);
-  if (many && chunks <= 64) return launch_norm_rows<2, POW2>(a, stream);
+  // Chunks per thread: one while there are no more than 512 threads' worth of them
+  // per SM (latency: 1 x 2048 2.1 us with one, 2.4 with two, 2.7 with four; 200 x
+  // 2048 2.5, 2.7, 3.2), two up to 1024 (512 x 2048 3.9, 3.4, 3.8), then four (64
+  // registers, and more loads in flight per thread: 16384 x 2048 45.8, 40.1, 39.6
+  // and 39.9 us with eight; 333 x 8192 7.8, 6.1, 4.9, 5.8). Rows of more than 512
+  // chunks never have one (148 x 8192 5.4, 3.9, 4.1), short ones no more than keep
+  // a warp busy.
+  const int64_t total = a.rows_pad * chunks;
+  const int64_t v = total > 1024 * dev.sm_count                     ? 4
+                    : total > 512 * dev.sm_count || chunks > 512 ? 2
+                                                                    : 1;
+  if (v == 1 || chunks <= 32) return launch_norm_rows<1, POW2>(a, stream);
+  if ((v == 2 && chunks <= 1024) || chunks <= 64) return launch_norm_rows<2, POW2>(a, stream);
   if (chunks <= 2048) return launch_norm_rows<4, POW2>(a, stream);
   return launch_norm_rows<8, POW2>(a, stream);
 }
