@@ -46,7 +46,9 @@ extern "C" {
  *   y           : bf16 [rows, cols] (out) or NULL: v rounded to bf16
  *   q, s        : row-wise codes of v (out), both or neither
  *   q_t, s_t    : column-wise codes of v, transposed (out), both or neither
- * cols <= 32768; eps >= 0 (else FP8BW_ERR_SHAPE). */
+ * cols <= 32768; eps >= 0 (else FP8BW_ERR_SHAPE). The sum of squares is fp32: a
+ * row in which it overflows (values around 2^63 and more) has rstd 0; a row of
+ * zeros with eps == 0 is not finite, as the formula says. */
 int fp8bw_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual,
                            const void* gamma, int gamma_is_f32, int64_t rows,
                            int64_t cols, float eps, uint16_t* h, float* rstd,
@@ -107,8 +109,9 @@ int fp8bw_swiglu_backward_quantize_pow2(const uint16_t* da, const uint16_t* gu,
  * rule of the Muon optimiser), for up to 8 matrices of any shapes at once:
  *   X = G / (||G||_F + eps), then `steps` times
  *   X <- a X + b (X X^T) X + c (X X^T)^2 X
- * (grouped on the shorter side). The products' operands are fp16 with fp32
- * accumulation; X itself is held in 32 bits. The polynomial must keep the
+ * (grouped on the shorter side; two consecutive steps may be taken as one there).
+ * The products' operands are fp16 with fp32 accumulation; X itself is held in 32
+ * bits, an fp16 pair (entries below 2^-45 are lost). The polynomial must keep the
  * singular values of X below 4 and those of b A + c A^2 (A = X X^T) below 15,
  * as the usual coefficients (3.4445, -4.7750, 2.0315) do: beyond, fp16
  * overflows and the result is not finite.
