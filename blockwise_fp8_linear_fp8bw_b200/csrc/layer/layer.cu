@@ -159,14 +159,14 @@ int allow_smem(DevicePrep& prep, int dev, K kernel, int bytes) {
 // ---------------------------------------------------------------- norm
 int threads_per_row(int64_t chunks, int v) { return static_cast<int>(cdiv(cdiv(chunks, v), 32) * 32); }
 
-template <int V, bool POW2>
+template <int V, int R, bool POW2>
 int launch_norm_rows(NormArgs a, cudaStream_t stream) {
   a.tpr = threads_per_row(a.cols / 8, V);
   const int groups = std::max(1, 256 / a.tpr);
-  const int64_t blocks = cdiv(a.rows_pad, groups);
+  const int64_t blocks = cdiv(a.rows_pad, groups * R);
   const auto kernel = a.cols == 8 * static_cast<int64_t>(V) * a.tpr
-                          ? rmsnorm_row_kernel<V, true, POW2>
-                          : rmsnorm_row_kernel<V, false, POW2>;
+                          ? rmsnorm_row_kernel<V, R, true, POW2>
+                          : rmsnorm_row_kernel<V, R, false, POW2>;
   return launched(launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(groups * a.tpr),
                                 0, stream, a));
 }
@@ -176,19 +176,23 @@ int norm_rows(const NormArgs& a, const Device& dev, cudaStream_t stream) {
   const int64_t chunks = a.cols / 8;
   // Chunks per thread: one while there are no more than 512 threads' worth of them
   // per SM (latency: 1 x 2048 2.1 us with one, 2.4 with two, 2.7 with four; 200 x
-  // 2048 2.5, 2.7, 3.2), two up to 1024 (512 x 2048 3.9, 3.4, 3.8), then four (64
-  // registers, and more loads in flight per thread: 16384 x 2048 45.8, 40.1, 39.6
-  // and 39.9 us with eight; 333 x 8192 7.8, 6.1, 4.9, 5.8). Rows of more than 512
-  // chunks never have one (148 x 8192 5.4, 3.9, 4.1), short ones no more than keep
-  // a warp busy.
+  // 2048 2.5, 2.7, 3.2), two up to 1024 (512 x 2048 3.9, 3.4, 3.8), then four, for
+  // loads in flight: as two chunks of two rows, which leaves fewer threads idle than
+  // four of one row (16384 x 2048 39.1 and 39.6 us, 45.8 with one chunk and 39.9 with
+  // eight; 16384 x 1040 24.5, 27.4, 29.6), of one row where a block would have to be
+  // larger (4096 x 8192 41.3, 40.4), and one of four rows in short ones (16384 x 128
+  // 6.6, 10.8, 5.1). Rows of more than 512 chunks never have one (148 x 8192 5.4, 3.9
+  // with two, 4.1 with four).
   const int64_t total = a.rows_pad * chunks;
-  const int64_t v = total > 1024 * dev.sm_count                     ? 4
-                    : total > 512 * dev.sm_count || chunks > 512 ? 2
-                                                                    : 1;
-  if (v == 1 || chunks <= 32) return launch_norm_rows<1, POW2>(a, stream);
-  if ((v == 2 && chunks <= 1024) || chunks <= 64) return launch_norm_rows<2, POW2>(a, stream);
-  if (chunks <= 2048) return launch_norm_rows<4, POW2>(a, stream);
-  return launch_norm_rows<8, POW2>(a, stream);
+  if (total > 1024 * dev.sm_count) {
+    if (chunks <= 32) return launch_norm_rows<1, 4, POW2>(a, stream);
+    if (chunks <= 512) return launch_norm_rows<2, 2, POW2>(a, stream);
+  } else {
+    if (total <= 512 * dev.sm_count && chunks <= 512) return launch_norm_rows<1, 1, POW2>(a, stream);
+    if (chunks <= 1024) return launch_norm_rows<2, 1, POW2>(a, stream);
+  }
+  if (chunks <= 2048) return launch_norm_rows<4, 1, POW2>(a, stream);
+  return launch_norm_rows<8, 1, POW2>(a, stream);
 }
 
 template <bool POW2>

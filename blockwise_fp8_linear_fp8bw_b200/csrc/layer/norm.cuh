@@ -123,14 +123,15 @@ __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
                     add_bf16x2(a.w, b.w));
 }
 
-// V chunks of 8 columns per thread; blockDim = groups x tpr, one row each.
+// R rows x V chunks of 8 columns per thread; blockDim = groups x tpr, R rows each.
 // FULL: the row is exactly V x tpr chunks. h * gamma and the groups' maxima of
 // it are formed before rstd is known, so all that is left after the row sum is
 // one product per element: codes are E4M3(h gamma * (rstd * qscale)).
-template <int V, bool FULL, bool POW2>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512)
+template <int V, int R, bool FULL, bool POW2>
+__global__ void __launch_bounds__(V * R == 1 ? 1024 : 512)
     rmsnorm_row_kernel(const NormArgs a) {
-  __shared__ float part[kNormMaxWarps];
+  constexpr int N = V * R;                     // item i: chunk i / R of row i % R
+  __shared__ float part[kNormMaxWarps][R];
   launch_dependents();
   grid_dependency_wait();
   const int tpr = a.tpr;
@@ -138,52 +139,58 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
   const int t = threadIdx.x - grp * tpr;
   const int groups = blockDim.x / tpr;
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * groups + grp;
-  const bool live = row < a.rows;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + grp) * R;
   const int chunks = static_cast<int>(a.cols >> 3);
-  const int64_t base = row * a.cols;
-  auto has = [&](int v) { return FULL || t + v * tpr < chunks; };
-  auto col = [&](int v) { return 8 * static_cast<int64_t>(t + v * tpr); };
+  const int64_t base = row0 * a.cols + 8 * t;
+  auto has = [&](int i) { return FULL || t + i / R * tpr < chunks; };
+  auto live = [&](int i) { return row0 + i % R < a.rows; };
+  auto at = [&](int i) { return base + i % R * a.cols + 8 * (i / R * tpr); };
 
-  uint4 h[V];
+  uint4 h[N];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    h[v] = live && has(v) ? ld16_stream(a.x + base + col(v)) : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < N; ++i)
+    h[i] = live(i) && has(i) ? ld16_stream(a.x + at(i)) : make_uint4(0u, 0u, 0u, 0u);
   if (a.residual != nullptr) {
-    uint4 r[V];
+    uint4 r[N];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      r[v] = live && has(v) ? ld16_stream(a.residual + base + col(v)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < N; ++i)
+      r[i] = live(i) && has(i) ? ld16_stream(a.residual + at(i)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = add_bf16x8(h[v], r[v]);
-      if (live && has(v)) *reinterpret_cast<uint4*>(a.h + base + col(v)) = h[v];
+    for (int i = 0; i < N; ++i) {
+      h[i] = add_bf16x8(h[i], r[i]);
+      if (live(i) && has(i)) *reinterpret_cast<uint4*>(a.h + at(i)) = h[i];
     }
   }
 
-  float ss = 0.0f, y[V][8], m[V];
+  float ss[R], y[N][8], m[N];
+#pragma unroll
+  for (int r = 0; r < R; ++r) ss[r] = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     float g[8];
-    if (has(v)) load_gamma8(a.gamma, a.gamma_f32, col(v), g);
+    if (has(v * R)) load_gamma8(a.gamma, a.gamma_f32, 8 * static_cast<int64_t>(t + v * tpr), g);
     else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = 0.0f;
     }
-    unpack8(h[v], y[v]);
-    m[v] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      ss = fmaf(y[v][j], y[v][j], ss);
-      ss = fmaf(y[v][j + 1], y[v][j + 1], ss);
-      fmul2(y[v][j], y[v][j + 1], y[v][j], y[v][j + 1], g[j], g[j + 1]);
-      m[v] = max3_abs(m[v], y[v][j], y[v][j + 1]);
+    for (int r = 0; r < R; ++r) {
+      const int i = v * R + r;
+      unpack8(h[i], y[i]);
+      m[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        ss[r] = fmaf(y[i][j], y[i][j], ss[r]);
+        ss[r] = fmaf(y[i][j + 1], y[i][j + 1], ss[r]);
+        fmul2(y[i][j], y[i][j + 1], y[i][j], y[i][j + 1], g[j], g[j + 1]);
+        m[i] = max3_abs(m[i], y[i][j], y[i][j + 1]);
+      }
     }
   }
   // group maxima over the 16 lanes of a half-warp: lanes halve the groups they
-  // hold as they exchange, so that each ends up with one of the V
+  // hold as they exchange, so that each ends up with one of the N
 #pragma unroll
-  for (int half = V / 2, bit = 8; bit >= 1; bit >>= 1) {
+  for (int half = N / 2, bit = 8; bit >= 1; bit >>= 1) {
     if (half >= 1) {
       const bool up = (lane & bit) != 0;
 #pragma unroll
@@ -197,51 +204,64 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
       m[0] = fmaxf(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], bit));
     }
   }
-  constexpr int kShare = 16 / V;               // lanes that hold the same group
+  constexpr int kShare = 16 / N;               // lanes that hold the same group
   const int mine = (lane & 15) / kShare;       // which one
 
-  ss = warp_sum(ss);
+#pragma unroll
+  for (int r = 0; r < R; ++r) ss[r] = warp_sum(ss[r]);
   const int wpr = tpr >> 5;
   if (wpr > 1) {
-    if (lane == 0) part[threadIdx.x >> 5] = ss;
-    __syncthreads();
-    ss = 0.0f;
-    for (int w = 0; w < wpr; ++w) ss += part[grp * wpr + w];
-  }
-  const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps));
-  if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
-
-  if (a.y != nullptr && live) {
+    if (lane == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!has(v)) continue;
+      for (int r = 0; r < R; ++r) part[threadIdx.x >> 5][r] = ss[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) ss[r] = 0.0f;
+    for (int w = 0; w < wpr; ++w) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) ss[r] += part[grp * wpr + w][r];
+    }
+  }
+  float rstd[R], my_rstd = 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    rstd[r] = __frcp_rn(__fsqrt_rn(__fdiv_rn(ss[r], static_cast<float>(a.cols)) + a.eps));
+    if (live(r) && t == 0 && a.rstd != nullptr) a.rstd[row0 + r] = rstd[r];
+    if (mine % R == r) my_rstd = rstd[r];
+  }
+
+  if (a.y != nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!live(i) || !has(i)) continue;
       uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_bf16(y[v][2 * j] * rstd, y[v][2 * j + 1] * rstd);
-      *reinterpret_cast<uint4*>(a.y + base + col(v)) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack_bf16(y[i][2 * j] * rstd[i % R], y[i][2 * j + 1] * rstd[i % R]);
+      *reinterpret_cast<uint4*>(a.y + at(i)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   if (a.q == nullptr) return;
   float qs, s;
-  scale_near<POW2>(m[0] * rstd, qs, s);
-  float f = qs * rstd;
+  scale_near<POW2>(m[0] * my_rstd, qs, s);
+  float f = qs * my_rstd;
   if constexpr (!POW2) {
     // rstd cancels: 448 / max|h gamma|, three roundings fewer (not where a scale of
     // 1 stands for none, or something is not finite)
     const float d = near_448_over(m[0]);
-    if (isfinite(d) && isfinite(rstd) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) f = d;
+    if (isfinite(d) && isfinite(my_rstd) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) f = d;
   }
-  const bool out = row < a.rows_pad;
-  const int64_t first = (t & ~15) + mine * tpr;       // first chunk of this lane's group
-  if ((lane & (kShare - 1)) == 0 && out && (FULL || first < chunks))
-    a.s[(first >> 4) * a.rows_pad + row] = s;
+  const int64_t first = (t & ~15) + mine / R * tpr;   // first chunk of this lane's group
+  if ((lane & (kShare - 1)) == 0 && row0 + mine % R < a.rows_pad && (FULL || first < chunks))
+    a.s[(first >> 4) * a.rows_pad + row0 + mine % R] = s;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float k = __shfl_sync(0xFFFFFFFFu, f, (lane & 16) | (v * kShare));
+  for (int i = 0; i < N; ++i) {
+    const float k = __shfl_sync(0xFFFFFFFFu, f, (lane & 16) | (i * kShare));
     uint2 w;
-    w.x = encode4(y[v][0], y[v][1], y[v][2], y[v][3], k);
-    w.y = encode4(y[v][4], y[v][5], y[v][6], y[v][7], k);
-    if (out && has(v)) *reinterpret_cast<uint2*>(a.q + base + col(v)) = w;
+    w.x = encode4(y[i][0], y[i][1], y[i][2], y[i][3], k);
+    w.y = encode4(y[i][4], y[i][5], y[i][6], y[i][7], k);
+    if (row0 + i % R < a.rows_pad && has(i)) *reinterpret_cast<uint2*>(a.q + at(i)) = w;
   }
 }
 
