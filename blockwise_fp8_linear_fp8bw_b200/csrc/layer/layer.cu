@@ -260,7 +260,8 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
 }
 
 // ---------------------------------------------------------------- norm, backward
-constexpr int64_t kBwdMaxBlocks = 296;    // two per SM of 148
+constexpr int64_t kBwdSms = 148;      // (the workspace's size must not ask the device)
+constexpr int kBwdSmThreads = 512;    // of 128 registers
 
 struct BwdPlan {
   int v, r, tpr, groups;
@@ -268,15 +269,21 @@ struct BwdPlan {
 };
 
 // The fewest chunks per thread that fit a row into 512 threads; two rows (or two
-// chunks) per thread and iteration, the next ones loading meanwhile.
+// chunks) per thread and iteration, the next ones loading meanwhile. Blocks of
+// about 128 threads or a row, as many as an SM's registers hold (16384 x 1040, 160
+// threads: 30.4 us with three per SM, 36.2 with two; 16384 x 528 18.9 and with 256
+// threads 20.0), but no more than the iterations need: a partial sum costs the last
+// kernel time (1037 x 1040: 6.3 us with 260 of them, 7.3 with 444).
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   BwdPlan p;
   const int64_t chunks = cols / 8;
   p.v = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
   p.r = p.v == 1 ? 2 : 1;
   p.tpr = threads_per_row(chunks, p.v);
-  p.groups = std::max(1, 256 / std::max(p.tpr, 1));
-  p.blocks = std::min<int64_t>(kBwdMaxBlocks, cdiv(rows, static_cast<int64_t>(p.groups) * p.r));
+  p.groups = std::max(1, 128 / std::max(p.tpr, 1));
+  const int64_t steps = cdiv(rows, static_cast<int64_t>(p.groups) * p.r);
+  const int64_t most = kBwdSms * std::max(1, kBwdSmThreads / std::max(p.groups * p.tpr, 1));
+  p.blocks = cdiv(steps, std::max<int64_t>(1, cdiv(steps, most)));
   p.parts = p.blocks * p.groups;
   return p;
 }
