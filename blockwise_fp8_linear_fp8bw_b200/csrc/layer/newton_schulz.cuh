@@ -235,7 +235,10 @@ __device__ __forceinline__ void tile_at(const Job& job, int lt, int& tm, int& tn
 // memory, so that rows of 64 bytes are read and written eight at a time (lanes
 // reading C row by row: 1.5% slower). The
 // product of a whole tile stays in TMEM (512 / BN tiles fit), so the epilogue
-// of one tile runs under the MMAs of the next.
+// of one tile runs under the MMAs of the next. Eight 2048 x 2048 matrices, five
+// steps: 1.65 ms, 833 TF/s of symmetric-half flops, bound by the operand feed (see
+// Maps) beside the reading and writing of hi and lo, and by the power limit when
+// hot (1.48 ms cold).
 template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ns_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args args) {

@@ -92,8 +92,8 @@ struct GluTileArgs {
 };
 
 // Forward: two tiles per step, half the columns apart, so that the barriers of a
-// step stand beside twice the work (113 us at 16384 x 6144 with one tile per
-// step, in two blocks per SM).
+// step stand beside twice the work (16384 x 6144: 109 us, 5.6 TB/s; 113 with one
+// tile per step, in two blocks per SM).
 constexpr int kGluFwdSlots = 6;
 using GluFwdRing = TileRing<4, kGluFwdSlots>;      // gate, up, twice
 struct GluFwdSmem {
@@ -167,7 +167,8 @@ __device__ __forceinline__ void glu_grad2(const float* g, const float* u, const 
 }
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
-// two halves): gate, up and da tiles in, a dgate and a dup tile out.
+// two halves): gate, up and da tiles in, a dgate and a dup tile out (16384 x 6144:
+// 168 us, 6.1 TB/s).
 constexpr int kGluBwdSlots = 6;
 using GluBwdRing = TileRing<3, kGluBwdSlots>;
 struct GluBwdSmem {
