@@ -201,7 +201,7 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
                      float* rstd, uint16_t* y, uint8_t* q, float* s, uint8_t* q_t, float* s_t,
                      void* stream) {
   if (rows < 0 || rows > kMaxRows || !cols_ok(cols, kMaxNormCols)) return FP8BW_ERR_SHAPE;
-  if (q_t != nullptr && cdiv(rows, 128) * cdiv(cols, kNormColTile) > INT32_MAX)
+  if (q_t != nullptr && cdiv(rows, 128) * cdiv(cols, kColTile) > INT32_MAX)
     return FP8BW_ERR_SHAPE;
   if (!(eps >= 0.0f)) return FP8BW_ERR_SHAPE;
   const int64_t rp = pad16(rows), n = rows * cols;
@@ -251,12 +251,12 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
   c.rows_pad = rp;
   c.cols = cols;
   c.tiles_r = static_cast<int>(cdiv(rp, 128));
-  c.tiles_c = static_cast<int>(cdiv(cols, kNormColTile));
+  c.tiles_c = static_cast<int>(cdiv(cols, kColTile));
   c.q_t = q_t;
   c.s_t = s_t;
   const int64_t tiles = static_cast<int64_t>(c.tiles_r) * c.tiles_c;
   return launched(launch_kernel(norm_col_kernel<POW2>, dim3(static_cast<unsigned>(tiles)),
-                                dim3(kNormColThreads), 0, cs, c));
+                                dim3(kColThreads), 0, cs, c));
 }
 
 // ---------------------------------------------------------------- norm, backward
@@ -336,6 +336,23 @@ bool glu_shape_ok(int64_t rows, int64_t f) {
          cdiv(rows, 128) * cdiv(2 * f, 128) <= INT32_MAX;
 }
 
+// 128 x 128 tiles of an output (they fit 31 bits: glu_shape_ok)
+int glu_tiles(const CodesOut& out) {
+  return static_cast<int>(cdiv(out.rows, kTile) * cdiv(out.cols, kTile));
+}
+
+template <bool POW2, bool BWD>
+int launch_glu_few(const uint16_t* gu, const uint16_t* da, int64_t rows, int64_t f,
+                   const CodesOut& out, cudaStream_t stream) {
+  const int64_t row_blocks = out.rows / 16 * cdiv(out.cols, kTile);
+  const int64_t tiles_c = cdiv(out.cols, kColTile);
+  const int64_t tiles = cdiv(out.rows, kTile) * tiles_c;
+  const GluFewArgs a{gu, da, rows, f, out, static_cast<int>(row_blocks), static_cast<int>(tiles_c)};
+  return launched(launch_kernel(swiglu_few_kernel<POW2, BWD>,
+                                dim3(static_cast<unsigned>(row_blocks + tiles)), dim3(kColThreads),
+                                0, stream, a));
+}
+
 template <bool POW2>
 int swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, float* s,
                     uint8_t* q_t, float* s_t, void* stream) {
@@ -354,13 +371,14 @@ int swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, flo
   st = current_device(&dev);
   if (st != FP8BW_OK || n == 0) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (q_t == nullptr) {
-    const GluRowArgs a{gu, rows, rp, f, q, s};
+  const CodesOut out{q, s, q_t, s_t, rp, f};
+  if (q_t == nullptr)
     return launched(launch_kernel(swiglu_row_kernel<POW2>,
                                   dim3(static_cast<unsigned>(rp / 16),
                                        static_cast<unsigned>(cdiv(f, 128))),
-                                  dim3(kGluRowThreads), 0, cs, a));
-  }
+                                  dim3(kColThreads), 0, cs, GluFewArgs{gu, nullptr, rows, f, out}));
+  if (glu_tiles(out) <= dev.sm_count)
+    return launch_glu_few<POW2, false>(gu, nullptr, rows, f, out, cs);
   CUtensorMap mg, mu;
   st = encode_tiles(&mg, gu, rows, f, 4 * f);
   if (st == FP8BW_OK) st = encode_tiles(&mu, gu + f, rows, f, 4 * f);
@@ -369,7 +387,7 @@ int swiglu_quantize(const uint16_t* gu, int64_t rows, int64_t f, uint8_t* q, flo
   st = allow_smem(prep, dev.ordinal, swiglu_tile_kernel<POW2>, GluFwdSmem::kAlloc);
   if (st != FP8BW_OK) return st;
   const GluTileArgs a{static_cast<int>(cdiv(rp, 128)), static_cast<int>(cdiv(f, 128)),
-                      CodesOut{q, s, q_t, s_t, rp, f}};
+                      out};
   const int tiles = a.tiles_r * ((a.tiles_c + 1) / 2);     // pairs
   return launched(launch_kernel(swiglu_tile_kernel<POW2>, dim3(std::min(tiles, dev.sm_count)),
                                 dim3(kTileThreads), GluFwdSmem::kAlloc, cs, mg, mu, a));
@@ -397,13 +415,12 @@ int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t row
   const dim3 grid(std::min(tiles_r * tiles_c, dev.sm_count)), block(kTileThreads);
   const CodesOut out{q, s, q_t, s_t, rp, 2 * f};
   static DevicePrep prep[2];
-  // Few tiles (two blocks per SM hold all of d's): the kernel that takes each by
-  // itself. 1000 x 1360 7.8 us with it and 9.2 without, 1500 x 2000 15.5 and 14.
-  if (f % 128 != 0 && static_cast<int64_t>(tiles_r) * cdiv(2 * f, 128) <= 2 * dev.sm_count) {
+  if (glu_tiles(out) <= dev.sm_count)
+    return launch_glu_few<POW2, true>(gu, da, rows, f, out, cs);
+  if (f % 128 != 0 && glu_tiles(out) <= 2 * dev.sm_count) {
     const GluRaggedArgs r{gu, da, rows, f,
                           GluTileArgs{tiles_r, static_cast<int>(cdiv(2 * f, 128)), out}};
-    return launched(launch_kernel(swiglu_bwd_ragged_kernel<POW2>,
-                                  dim3(r.t.tiles_r * r.t.tiles_c), block,
+    return launched(launch_kernel(swiglu_bwd_ragged_kernel<POW2>, dim3(glu_tiles(out)), block,
                                   TileEmit<1, true, false>::kBytes + 128, cs, r));
   }
   CUtensorMap mg, mu, md;

@@ -266,9 +266,8 @@ __global__ void __launch_bounds__(V * R == 1 ? 1024 : 512)
 }
 
 // ---------------------------------------------------------------- forward, column-wise
-// y of a 128 x 64 tile of h, from the rows' rstd, to column-wise codes. Thread t of
-// 256 holds rows 8 * (t / 16) .. +7 and columns 4 * (t % 16) .. +3. A block does one
-// tile and four blocks share an SM: a tile is a chain of loads and barriers, and
+// y of a 128 x 64 tile of h, from the rows' rstd, to column-wise codes. A block does
+// one tile and four blocks share an SM: a tile is a chain of loads and barriers, and
 // the other blocks work meanwhile. (16384 x 2048, both passes: 58.6 us. When it was
 // 61, steps of one 512-thread block per SM over 128 x 128 tiles with a TMA ring took
 // 63 and persistent blocks that copy the next tile ahead 66.)
@@ -283,28 +282,23 @@ struct NormColArgs {
   float* s_t;
 };
 
-constexpr int kNormColTile = 64;
-constexpr int kNormColThreads = 256;
-
 template <bool POW2>
-__global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const NormColArgs a) {
-  __shared__ float red[kNormColThreads / 32][kNormColTile];
-  __shared__ float colq[kNormColTile];
-  __shared__ __align__(16) uint8_t T[kNormColTile * kTile];
+__global__ void __launch_bounds__(kColThreads, 4) norm_col_kernel(const NormColArgs a) {
+  __shared__ ColumnsSmem sm;
   launch_dependents();
   grid_dependency_wait();
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rb = t >> 4, cb = t & 15;
+  const int t = threadIdx.x, rb = t >> 4, cb = t & 15;
   // last rows first: they are the most recently written, and still in L2
   const int tile = a.tiles_r * a.tiles_c - 1 - static_cast<int>(blockIdx.x);
   const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
   const int64_t r0 = static_cast<int64_t>(tr) * kTile + rb * 8;
-  const int64_t c0 = static_cast<int64_t>(tc) * kNormColTile + cb * 4;
+  const int64_t c0 = static_cast<int64_t>(tc) * kColTile + cb * 4;
   // h * rstd; the norm weight joins a column's scale
   uint2 w[8];
   float rs[8];
   const uint16_t* h = a.h + r0 * a.cols + c0;
   if (static_cast<int64_t>(tr + 1) * kTile <= a.rows &&
-      static_cast<int64_t>(tc + 1) * kNormColTile <= a.cols) {
+      static_cast<int64_t>(tc + 1) * kColTile <= a.cols) {
     const float4 ra = reinterpret_cast<const float4*>(a.rstd + r0)[0];
     const float4 rc = reinterpret_cast<const float4*>(a.rstd + r0)[1];
     rs[0] = ra.x, rs[1] = ra.y, rs[2] = ra.z, rs[3] = ra.w;
@@ -329,45 +323,8 @@ __global__ void __launch_bounds__(kNormColThreads, 4) norm_col_kernel(const Norm
       for (int j = 0; j < 4; ++j) m[j] = max3_abs(m[j], y[p - 1][j], y[p][j]);
     }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
-  if (lane < 16) *reinterpret_cast<float4*>(&red[warp][cb * 4]) = make_float4(m[0], m[1], m[2], m[3]);
-  __syncthreads();
-  if (t < kNormColTile) {
-    const int64_t c = static_cast<int64_t>(tc) * kNormColTile + t;
-    const float g = c < a.cols ? load_gamma(a.gamma, a.gamma_f32, c) : 0.0f;
-    float am = red[0][t];
-#pragma unroll
-    for (int i = 1; i < kNormColThreads / 32; ++i) am = fmaxf(am, red[i][t]);
-    float qs, s;
-    scale_near<POW2>(am * fabsf(g), qs, s);
-    colq[t] = qs * g;
-    if (c < a.cols) a.s_t[static_cast<int64_t>(tr) * a.cols + c] = s;
-  }
-  __syncthreads();
-  const float4 k = *reinterpret_cast<const float4*>(&colq[cb * 4]);
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    fmul2(y[p][0], y[p][1], y[p][0], y[p][1], k.x, k.y);
-    fmul2(y[p][2], y[p][3], y[p][2], y[p][3], k.z, k.w);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint2*>(T + emit_t_offset(cb * 4 + j, rb)) =
-        make_uint2(e4m3x4(y[0][j], y[1][j], y[2][j], y[3][j]),
-                   e4m3x4(y[4][j], y[5][j], y[6][j], y[7][j]));
-  __syncthreads();
-  // tile column kk is 128 contiguous tokens of row tc*64 + kk of q_t
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int kk = i * 32 + (t >> 3), ch = t & 7;
-    const int64_t c = static_cast<int64_t>(tc) * kNormColTile + kk;
-    const int64_t tok = static_cast<int64_t>(tr) * kTile + ch * 16;
-    const uint2 lo = *reinterpret_cast<const uint2*>(T + emit_t_offset(kk, 2 * ch));
-    const uint2 hi = *reinterpret_cast<const uint2*>(T + emit_t_offset(kk, 2 * ch + 1));
-    if (c < a.cols && tok < a.rows_pad)
-      *reinterpret_cast<uint4*>(a.q_t + c * a.rows_pad + tok) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-  }
+  emit_columns<POW2>(sm, y, m, tr, tc, a.rows_pad, a.cols, a.q_t, a.s_t,
+                     [&](int64_t c) { return load_gamma(a.gamma, a.gamma_f32, c); });
 }
 
 // ---------------------------------------------------------------- backward

@@ -41,36 +41,67 @@ __device__ __forceinline__ void glu2(const float* g, const float* u, float* y) {
   fmul2(y[0], y[1], w0, w1, u[0], u[1]);
 }
 
-// ---------------------------------------------------------------- row-wise only
-struct GluRowArgs {
+// Two elements of the backward pass.
+__device__ __forceinline__ void glu_grad2(const float* g, const float* u, const float* d,
+                                          float* dgate, float* dup) {
+  float s0, s1, w0, w1, c0 = 1.0f, c1 = 1.0f;
+  sigmoid2(g[0], g[1], s0, s1);
+  fmul2(w0, w1, d[0], d[1], s0, s1);
+  fmul2(dup[0], dup[1], w0, w1, g[0], g[1]);
+  fmul2(w0, w1, w0, w1, u[0], u[1]);
+  ffma2(c0, c1, s0, s1, -1.0f, -1.0f);          // 1 - sg
+  float t0 = 1.0f, t1 = 1.0f;
+  ffma2(t0, t1, g[0], g[1], c0, c1);            // 1 + gate (1 - sg)
+  fmul2(dgate[0], dgate[1], w0, w1, t0, t1);
+}
+
+// ---------------------------------------------------------------- row-wise, or few tiles
+// BWD: d = [dgate | dup], else a. The row-wise part of an output takes a half-warp
+// per row and 1x128 group (a block: 16 rows of one group, so its scales are one
+// 64-byte run), the column-wise part a block per 128 x 64 tile; both in one launch,
+// each from inputs of its own (read twice, from L2). For no more than a tile per SM
+// that is quicker than the kernels below (us, here and there: 1 x 6144 2.1 and 6.7,
+// 100 x 1360 3.9 and 6.8, 1000 x 2048 6.3 and 7.1, 1000 x 4096 10.6 and 7.7; backward
+// 1 x 6144 2.4 and 5.6, 100 x 1360 4.3 and 5.3, 300 x 2048 5.5 and 6.0, 777 x 1360
+// 7.5 and 7.0).
+struct GluFewArgs {
   const uint16_t* gu;
-  int64_t rows, rows_pad, f;
-  uint8_t* q;
-  float* s;
+  const uint16_t* da;       // BWD
+  int64_t rows, f;
+  CodesOut out;
+  int row_blocks;           // the first ones; the others take tiles
+  int tiles_c;
 };
 
-constexpr int kGluRowThreads = 256;
+// The input columns of output column c of BWD.
+__device__ __forceinline__ int64_t glu_source(int64_t c, int64_t f) { return c >= f ? c - f : c; }
 
-// One half-warp per row and group; a block takes 16 rows of one group, so its
-// scales are one 64-byte run.
-template <bool POW2>
-__global__ void __launch_bounds__(kGluRowThreads) swiglu_row_kernel(const GluRowArgs a) {
-  launch_dependents();
-  grid_dependency_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * 128 + (threadIdx.x & 15) * 8;
-  const bool in = row < a.rows && c < a.f;
+// Rows 16 i .. 16 i + 15 of a 1x128 group, by 256 threads.
+template <bool POW2, bool BWD>
+__device__ __forceinline__ void glu_rows(const GluFewArgs& a, int64_t i, int64_t group) {
+  const int t = threadIdx.x;
+  const int64_t row = i * 16 + (t >> 4), c = group * kTile + (t & 15) * 8;
   float y[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-  if (in) {
-    const uint16_t* p = a.gu + row * 2 * a.f + c;
+  if (row < a.rows && c < a.out.cols) {
+    const int64_t src = BWD ? glu_source(c, a.f) : c;
+    const uint16_t* p = a.gu + row * 2 * a.f + src;
     const uint4 wg = ld16_stream(p), wu = ld16_stream(p + a.f);
     float g[8], u[8];
     unpack8(wg, g);
     unpack8(wu, u);
+    if constexpr (BWD) {
+      float d[8], dg[8], du[8];
+      unpack8(ld16_stream(a.da + row * a.f + src), d);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) glu2(g + j, u + j, y + j);
+      for (int j = 0; j < 8; j += 2) glu_grad2(g + j, u + j, d + j, dg + j, du + j);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = c >= a.f ? du[j] : dg[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) glu2(g + j, u + j, y + j);
+    }
   }
   float m = max3_abs(max3_abs(0.0f, y[0], y[1]), y[2], y[3]);
   m = max3_abs(max3_abs(m, y[4], y[5]), y[6], y[7]);
@@ -78,11 +109,68 @@ __global__ void __launch_bounds__(kGluRowThreads) swiglu_row_kernel(const GluRow
   for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float qs, s;
   scale_near<POW2>(m, qs, s);
-  if (row < a.rows_pad && c < a.f) {
-    *reinterpret_cast<uint2*>(a.q + row * a.f + c) =
+  if (c < a.out.cols)
+    *reinterpret_cast<uint2*>(a.out.q + row * a.out.cols + c) =
         make_uint2(encode4(y[0], y[1], y[2], y[3], qs), encode4(y[4], y[5], y[6], y[7], qs));
-    if ((threadIdx.x & 15) == 0) a.s[static_cast<int64_t>(blockIdx.y) * a.rows_pad + row] = s;
+  if ((t & 15) == 0) a.out.s[group * a.out.rows + row] = s;
+}
+
+template <bool POW2>
+__global__ void __launch_bounds__(kColThreads) swiglu_row_kernel(const GluFewArgs a) {
+  launch_dependents();
+  grid_dependency_wait();
+  glu_rows<POW2, false>(a, blockIdx.x, blockIdx.y);
+}
+
+template <bool POW2, bool BWD>
+__global__ void __launch_bounds__(kColThreads) swiglu_few_kernel(const GluFewArgs a) {
+  __shared__ ColumnsSmem sm;
+  launch_dependents();
+  grid_dependency_wait();
+  const int t = threadIdx.x;
+  if (static_cast<int>(blockIdx.x) < a.row_blocks) {
+    const int rb = static_cast<int>(a.out.rows / 16);
+    glu_rows<POW2, BWD>(a, blockIdx.x % rb, blockIdx.x / rb);
+    return;
   }
+  const int tile = static_cast<int>(blockIdx.x) - a.row_blocks;
+  const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
+  const int64_t r0 = static_cast<int64_t>(tr) * kTile + (t >> 4) * 8;
+  const int64_t c = static_cast<int64_t>(tc) * kColTile + (t & 15) * 4;
+  const int64_t src = BWD ? glu_source(c, a.f) : c;
+  float y[8][4], m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[p][j] = 0.0f;
+    if (r0 + p < a.rows && c < a.out.cols) {
+      const uint16_t* gp = a.gu + (r0 + p) * 2 * a.f + src;
+      const uint2 wg = *reinterpret_cast<const uint2*>(gp);
+      const uint2 wu = *reinterpret_cast<const uint2*>(gp + a.f);
+      const float g[4] = {bf16_lo(wg.x), bf16_hi(wg.x), bf16_lo(wg.y), bf16_hi(wg.y)};
+      const float u[4] = {bf16_lo(wu.x), bf16_hi(wu.x), bf16_lo(wu.y), bf16_hi(wu.y)};
+      if constexpr (BWD) {
+        const uint2 wd = *reinterpret_cast<const uint2*>(a.da + (r0 + p) * a.f + src);
+        const float d[4] = {bf16_lo(wd.x), bf16_hi(wd.x), bf16_lo(wd.y), bf16_hi(wd.y)};
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          float dg[2], du[2];
+          glu_grad2(g + j, u + j, d + j, dg, du);
+          y[p][j] = c >= a.f ? du[0] : dg[0];
+          y[p][j + 1] = c >= a.f ? du[1] : dg[1];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) glu2(g + j, u + j, &y[p][j]);
+      }
+    }
+    if (p & 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = max3_abs(m[j], y[p - 1][j], y[p][j]);
+    }
+  }
+  emit_columns<POW2>(sm, y, m, tr, tc, a.out.rows, a.out.cols, a.out.q_t, a.out.s_t,
+                     [](int64_t) { return 1.0f; });
 }
 
 // ---------------------------------------------------------------- 128x128 tiles
@@ -150,20 +238,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   emit.finish();
   if (threadIdx.x == 0) ring.drain();
-}
-
-// Two elements of the backward pass.
-__device__ __forceinline__ void glu_grad2(const float* g, const float* u, const float* d,
-                                          float* dgate, float* dup) {
-  float s0, s1, w0, w1, c0 = 1.0f, c1 = 1.0f;
-  sigmoid2(g[0], g[1], s0, s1);
-  fmul2(w0, w1, d[0], d[1], s0, s1);
-  fmul2(dup[0], dup[1], w0, w1, g[0], g[1]);
-  fmul2(w0, w1, w0, w1, u[0], u[1]);
-  ffma2(c0, c1, s0, s1, -1.0f, -1.0f);          // 1 - sg
-  float t0 = 1.0f, t1 = 1.0f;
-  ffma2(t0, t1, g[0], g[1], c0, c1);            // 1 + gate (1 - sg)
-  fmul2(dgate[0], dgate[1], w0, w1, t0, t1);
 }
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
@@ -371,10 +445,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) ring.drain();
 }
 
-// The same for few tiles: each tile of d's 2f columns by itself, every 4-column
-// run from its own gate, up and da columns (read twice in all, with plain loads),
-// in two blocks per SM. Half the work per block, and no second tile to wait for:
-// 777 x 1360 7.1 us against 8.7 above, 300 x 1360 6.2 and 8.8.
+// The same for no more tiles of d than two blocks per SM hold: each tile by itself,
+// every 4-column run from its own gate, up and da columns (read twice in all, with
+// plain loads). Half the work per block, and no second tile to wait for: 777 x 1360
+// 7.0 us against 8.7 above, 1000 x 1360 7.8 and 9.2.
 struct GluRaggedArgs {
   const uint16_t* gu;
   const uint16_t* da;

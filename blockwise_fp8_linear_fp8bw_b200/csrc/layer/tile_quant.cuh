@@ -291,6 +291,67 @@ struct TileEmit {
   }
 };
 
+// ---------------------------------------------------------------- columns alone
+// Column-wise codes of a 128 x 64 tile by 256 threads: thread t holds rows
+// 8 * (t / 16) .. +7 and columns 4 * (t % 16) .. +3.
+constexpr int kColTile = 64;
+constexpr int kColThreads = 256;
+
+struct ColumnsSmem {
+  float red[kColThreads / 32][kColTile];
+  float q[kColTile];
+  __align__(16) uint8_t t[kColTile * kTile];
+};
+
+// Of y times gain(column), from the thread's column maxima m of |y|; entries outside
+// the tensor must be zero.
+template <bool POW2, typename Gain>
+__device__ __forceinline__ void emit_columns(ColumnsSmem& sm, float (&y)[8][4], float (&m)[4],
+                                             int tr, int tc, int64_t rows_pad, int64_t cols,
+                                             uint8_t* q_t, float* s_t, Gain&& gain) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rb = t >> 4, cb = t & 15;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+  if (lane < 16)
+    *reinterpret_cast<float4*>(&sm.red[warp][cb * 4]) = make_float4(m[0], m[1], m[2], m[3]);
+  __syncthreads();
+  if (t < kColTile) {
+    const int64_t c = static_cast<int64_t>(tc) * kColTile + t;
+    const float g = c < cols ? gain(c) : 0.0f;
+    float am = sm.red[0][t];
+#pragma unroll
+    for (int i = 1; i < kColThreads / 32; ++i) am = fmaxf(am, sm.red[i][t]);
+    float qs, s;
+    scale_near<POW2>(am * fabsf(g), qs, s);
+    sm.q[t] = qs * g;
+    if (c < cols) s_t[static_cast<int64_t>(tr) * cols + c] = s;
+  }
+  __syncthreads();
+  const float4 k = *reinterpret_cast<const float4*>(&sm.q[cb * 4]);
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    fmul2(y[p][0], y[p][1], y[p][0], y[p][1], k.x, k.y);
+    fmul2(y[p][2], y[p][3], y[p][2], y[p][3], k.z, k.w);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint2*>(sm.t + emit_t_offset(cb * 4 + j, rb)) =
+        make_uint2(e4m3x4(y[0][j], y[1][j], y[2][j], y[3][j]),
+                   e4m3x4(y[4][j], y[5][j], y[6][j], y[7][j]));
+  __syncthreads();
+  // tile column kk is 128 contiguous tokens of row tc*64 + kk of q_t
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int kk = i * 32 + (t >> 3), ch = t & 7;
+    const int64_t c = static_cast<int64_t>(tc) * kColTile + kk;
+    const int64_t tok = static_cast<int64_t>(tr) * kTile + ch * 16;
+    const uint2 lo = *reinterpret_cast<const uint2*>(sm.t + emit_t_offset(kk, 2 * ch));
+    const uint2 hi = *reinterpret_cast<const uint2*>(sm.t + emit_t_offset(kk, 2 * ch + 1));
+    if (c < cols && tok < rows_pad)
+      *reinterpret_cast<uint4*>(q_t + c * rows_pad + tok) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+}
+
 // ---------------------------------------------------------------- input ring
 // A ring of SLOTS bf16 tiles, filled by thread 0 and read by all; the i-th step
 // of a block takes the NIN tiles i*NIN .. i*NIN+NIN-1 of its sequence. Every wait

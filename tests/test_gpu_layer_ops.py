@@ -32,7 +32,8 @@ def _normal(shape, seed, scale=1.0, dtype=None):
 
 ROWS_COLS = [(1, 16), (1, 2048), (2, 128), (15, 144), (16, 1040), (17, 2048),
              (127, 256), (129, 4096), (300, 8192), (5, 8208), (640, 8208),
-             (33, 16400), (700, 16400), (3, 32768), (1200, 272), (4100, 48)]
+             (33, 16400), (700, 16400), (3, 32768), (1200, 272), (4100, 48),
+             (90, 8192), (100, 6160), (1300, 1024), (1237, 1040), (5000, 256), (10005, 144)]
 
 
 @pytest.mark.parametrize("rows,cols", ROWS_COLS)
@@ -105,11 +106,14 @@ def test_norm_backward_against_differences():
 
 
 GLU_SIZES = [(1, 16), (1, 6144), (7, 144), (16, 128), (17, 256), (128, 640),
-             (129, 1360), (333, 272), (1000, 1024), (2050, 48)]
+             (129, 1360), (333, 272), (1000, 1024), (2050, 48), (1300, 2000),
+             (4100, 640), (2500, 1040)]
 # for the backward pass also widths whose end, over several rows of tiles per
 # block, is 16 to 112 columns past a multiple of 128
 GLU_BWD_SIZES = GLU_SIZES + [(6500, 464), (9000, 192), (4000, 720), (3000, 1296),
-                             (7000, 112), (2700, 880), (130, 80), (40, 2032)]
+                             (7000, 112), (2700, 880), (130, 80), (40, 2032),
+                             (15000, 192), (20001, 112), (40000, 48), (1100, 1360),
+                             (1300, 1024)]
 
 
 @pytest.mark.parametrize("rows,f", GLU_SIZES)
@@ -367,7 +371,8 @@ class _Guarded:
             assert bool((buf[:256] == 0xA5).all()) and bool((buf[256 + size:] == 0xA5).all())
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 272), (19, 1040), (131, 400), (300, 2064)])
+@pytest.mark.parametrize("rows,cols", [(1, 272), (19, 1040), (131, 400), (300, 2064),
+                                       (1111, 2064), (1100, 1200), (2400, 1280)])
 def test_nothing_is_written_outside_the_outputs(rows, cols):
     torch, ops = _t(), _ops()
     g = _Guarded()
