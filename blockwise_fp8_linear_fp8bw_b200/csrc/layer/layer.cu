@@ -264,27 +264,34 @@ constexpr int64_t kBwdSms = 148;      // (the workspace's size must not ask the 
 constexpr int kBwdSmThreads = 512;    // of 128 registers
 
 struct BwdPlan {
-  int v, r, tpr, groups;
-  int64_t blocks, parts;
+  int v, r, tpr, groups, per_sm;
+  int64_t blocks;
 };
 
-// The fewest chunks per thread that fit a row into 512 threads; two rows (or two
-// chunks) per thread and iteration, the next ones loading meanwhile. Blocks of
-// about 128 threads or a row, as many as an SM's registers hold (16384 x 1040, 160
-// threads: 30.4 us with three per SM, 36.2 with two; 16384 x 528 18.9 and with 256
-// threads 20.0), but no more than the iterations need: a partial sum costs the last
-// kernel time (1037 x 1040: 6.3 us with 260 of them, 7.3 with 444).
+// Chunks of a row per thread that fit it into 512 threads; up to 512 chunks the
+// choice of one chunk of two rows or two of one that has more of them on an SM, the
+// next ones loading meanwhile (16384 x 2064: 258 chunks, one block of 288 threads per
+// SM or three of 160). Blocks of about 128 threads or a row, as many as an SM's
+// registers hold (16384 x 1040, 160 threads: 30.4 us with three per SM, 36.2 with
+// two; 16384 x 528 18.9 and with 256 threads 20.0), but no more than the iterations
+// need: a partial sum costs the last kernel time (1037 x 1040: 6.3 us with 260 of
+// them, 7.3 with 444).
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
-  BwdPlan p;
   const int64_t chunks = cols / 8;
-  p.v = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
-  p.r = p.v == 1 ? 2 : 1;
-  p.tpr = threads_per_row(chunks, p.v);
-  p.groups = std::max(1, 128 / std::max(p.tpr, 1));
+  auto plan = [&](int v) {
+    BwdPlan p;
+    p.v = v;
+    p.r = v == 1 ? 2 : 1;
+    p.tpr = threads_per_row(chunks, v);
+    p.groups = std::max(1, 128 / std::max(p.tpr, 1));
+    p.per_sm = std::max(1, kBwdSmThreads / std::max(p.groups * p.tpr, 1));
+    return p;
+  };
+  auto in_flight = [](const BwdPlan& p) { return p.per_sm * p.groups * p.r; };   // rows
+  BwdPlan p = plan(chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8);
+  if (p.v == 1 && in_flight(plan(2)) > in_flight(p)) p = plan(2);
   const int64_t steps = cdiv(rows, static_cast<int64_t>(p.groups) * p.r);
-  const int64_t most = kBwdSms * std::max(1, kBwdSmThreads / std::max(p.groups * p.tpr, 1));
-  p.blocks = cdiv(steps, std::max<int64_t>(1, cdiv(steps, most)));
-  p.parts = p.blocks * p.groups;
+  p.blocks = cdiv(steps, std::max<int64_t>(1, cdiv(steps, kBwdSms * p.per_sm)));
   return p;
 }
 
@@ -293,7 +300,7 @@ int rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd, c
                      uint16_t* dh, float* dgamma, void* ws, int64_t ws_bytes, void* stream) {
   if (rows < 0 || rows > kMaxRows || !cols_ok(cols, kMaxNormCols)) return FP8BW_ERR_SHAPE;
   const int64_t n = rows * cols;
-  const int64_t need = n > 0 ? bwd_plan(rows, cols).parts * cols * 4 : 0;
+  const int64_t need = n > 0 ? bwd_plan(rows, cols).blocks * cols * 4 : 0;
   if (ws_bytes < need) return FP8BW_ERR_SHAPE;
   Buffers b;
   b.in(dy, 2 * n);
@@ -325,9 +332,15 @@ int rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd, c
   st = launched(launch_kernel(kernel, dim3(static_cast<unsigned>(p.blocks)),
                               dim3(p.groups * p.tpr), 0, cs, a));
   if (st != FP8BW_OK) return st;
-  return launched(launch_kernel(dgamma_reduce_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32))),
-                                dim3(1024), 0, cs, static_cast<const float*>(ws), p.parts, cols,
-                                dgamma));
+  // Eight columns per block where 32 would leave few blocks with long slices (us, with
+  // 8 and with 32: 1907 x 128 4.5 and 5.5, 778 x 320 4.7 and 5.8, 933 x 944 6.5 and
+  // 7.2; but 1037 x 1040, of 260 partial sums, 6.6 and 6.4)
+  const float* part = static_cast<const float*>(ws);
+  if (cols <= (p.blocks > 288 ? 2048 : 1024))
+    return launched(launch_kernel(dgamma_reduce_kernel<8>, dim3(static_cast<unsigned>(cdiv(cols, 8))),
+                                  dim3(1024), 0, cs, part, p.blocks, cols, dgamma));
+  return launched(launch_kernel(dgamma_reduce_kernel<32>, dim3(static_cast<unsigned>(cdiv(cols, 32))),
+                                dim3(1024), 0, cs, part, p.blocks, cols, dgamma));
 }
 
 // ---------------------------------------------------------------- gated product
@@ -853,7 +866,7 @@ int fp8bw_rmsnorm_quantize_pow2(const uint16_t* x, const uint16_t* residual, con
 int64_t fp8bw_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || rows > layer::kMaxRows || !layer::cols_ok(cols, layer::kMaxNormCols))
     return FP8BW_ERR_SHAPE;
-  return rows * cols > 0 ? layer::bwd_plan(rows, cols).parts * cols * 4 : 0;
+  return rows * cols > 0 ? layer::bwd_plan(rows, cols).blocks * cols * 4 : 0;
 }
 
 int fp8bw_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const float* rstd,

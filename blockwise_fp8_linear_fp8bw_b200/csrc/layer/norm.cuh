@@ -337,7 +337,7 @@ struct NormBwdArgs {
   const uint16_t* dres;       // may be null
   int64_t rows, cols;
   uint16_t* dh;
-  float* part;                // [gridDim.x * groups][cols] partial dgamma
+  float* part;                // [gridDim.x][cols] partial dgamma
   int tpr;
 };
 
@@ -496,7 +496,28 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
       load_rows(b + bstep, dy, h, dr, rs);
     }
   }
-  float* out = a.part + (static_cast<int64_t>(blockIdx.x) * groups + grp) * a.cols;
+  if constexpr (V == 1) {
+    // the groups' sums, one after another (blocks of several groups have up to 128
+    // threads)
+    if (groups > 1) {
+      __shared__ float4 sums[128][2];
+      if (grp > 0) {
+        sums[threadIdx.x][0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+        sums[threadIdx.x][1] = make_float4(acc[0][4], acc[0][5], acc[0][6], acc[0][7]);
+      }
+      __syncthreads();
+      if (grp > 0) return;
+      for (int g = 1; g < groups; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 s = sums[g * tpr + t][i];
+          acc[0][4 * i] += s.x, acc[0][4 * i + 1] += s.y;
+          acc[0][4 * i + 2] += s.z, acc[0][4 * i + 3] += s.w;
+        }
+      }
+    }
+  }
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = t + v * tpr;
@@ -507,22 +528,27 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const NormBwdArgs a
   }
 }
 
-// dgamma[c] = sum over the partial rows, in a fixed order (32 slices, then the
-// slices one after another): the same bits for the same inputs every time.
+// dgamma[c] = sum over the partial rows, in a fixed order (slices, a warp's, then the
+// warps one after another): the same bits for the same inputs every time. A block
+// takes C columns in 1024 / C slices of the rows: few columns for narrow norms, whose
+// blocks would otherwise be few and their slices long.
+template <int C>
 __global__ void __launch_bounds__(1024)
     dgamma_reduce_kernel(const float* part, int64_t nparts, int64_t cols, float* dgamma) {
-  __shared__ float sum[32][33];
+  __shared__ float sum[32][C + 1];
   launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * C + lane % C;
   float s = 0.0f;
   if (c < cols)
 #pragma unroll 8
-    for (int64_t p = slice; p < nparts; p += 32) s += part[p * cols + c];
-  sum[slice][lane] = s;
+    for (int64_t p = threadIdx.x / C; p < nparts; p += 1024 / C) s += part[p * cols + c];
+#pragma unroll
+  for (int o = C; o < 32; o *= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane < C) sum[warp][lane] = s;
   __syncthreads();
-  if (slice == 0 && c < cols) {
+  if (warp == 0 && lane < C && c < cols) {
     float r = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) r += sum[i][lane];
