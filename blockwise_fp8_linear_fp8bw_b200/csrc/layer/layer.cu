@@ -234,6 +234,7 @@ int rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void* ga
   a.rows = rows;
   a.rows_pad = rp;
   a.cols = cols;
+  a.inv_cols = 1.0 / static_cast<double>(cols);
   a.eps = eps;
   a.h = h;
   a.rstd = rstd;

@@ -101,6 +101,7 @@ struct NormArgs {
   const void* gamma;
   int gamma_f32;
   int64_t rows, rows_pad, cols;
+  double inv_cols;
   float eps;
   uint16_t* h;                // written when there is a residual
   float* rstd;                // may be null
@@ -111,6 +112,15 @@ struct NormArgs {
 };
 
 constexpr int kNormMaxWarps = 32;
+
+// 1 / sqrt(sum / cols + eps), rounded once: its error is in every value of the row.
+// The approximate root and one Newton step in 64 bits (not from zero or infinity).
+__device__ __forceinline__ float rsqrt_of_mean(float sum, double inv_cols, float eps) {
+  const double x = fma(static_cast<double>(sum), inv_cols, static_cast<double>(eps));
+  const float r = rsqrtf(static_cast<float>(x));
+  const double d = r, n = d * fma(-0.5 * x * d, d, 1.5);
+  return r > 0.0f && r < 1e30f ? static_cast<float>(n) : r;
+}
 
 // Element-wise bf16 sums of two packed vectors, each rounded once.
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(V * R == 1 ? 1024 : 512)
   float rstd[R], my_rstd = 0.0f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    rstd[r] = __frcp_rn(__fsqrt_rn(__fdiv_rn(ss[r], static_cast<float>(a.cols)) + a.eps));
+    rstd[r] = rsqrt_of_mean(ss[r], a.inv_cols, a.eps);
     if (live(r) && t == 0 && a.rstd != nullptr) a.rstd[row0 + r] = rstd[r];
     if (mine % R == r) my_rstd = rstd[r];
   }

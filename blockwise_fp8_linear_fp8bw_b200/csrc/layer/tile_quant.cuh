@@ -62,21 +62,26 @@ __device__ __forceinline__ float max3_abs(float m, float a, float b) {
   return r;
 }
 
-// 448 / amax within 2 ulp: the approximate reciprocal and one Newton step (of
-// amax / 16, so that no finite amax has a subnormal reciprocal). 0 for infinity,
-// infinite or NaN where the quotient is.
+// 448 / amax within an ulp: the approximate reciprocal (of amax / 16, so that no
+// finite amax has a subnormal one) and a correction by what the product leaves of
+// 448. 0 for infinity, infinite or NaN where the quotient is.
 __device__ __forceinline__ float near_448_over(float amax) {
-  const float a = amax * 0.0625f;
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
-  const float e = fmaf(-a, r, 1.0f);
-  return 28.0f * (fabsf(e) < 1.0f ? fmaf(r, e, r) : r);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * 0.0625f));
+  const float q = 28.0f * r, e = fmaf(-q, amax, 448.0f);
+  return fabsf(e) < 1.0f ? fmaf(e * 0.0625f, r, q) : q;
 }
 
-// scale_of for the fused kernels: the quotients are within 2 ulp instead of
+// amax / 448, corrected in the same way.
+__device__ __forceinline__ float near_over_448(float amax) {
+  const float q = amax * (1.0f / 448.0f);
+  return isfinite(amax) ? fmaf(fmaf(-q, 448.0f, amax), 1.0f / 448.0f, q) : q;
+}
+
+// scale_of for the fused kernels: the quotients are within an ulp instead of
 // correctly rounded (two IEEE divisions cost some 40 instructions and their
 // latency, in every step). amax still encodes as 448, and other codes differ only
-// for values within 2^-21 of a tie.
+// for values within 2^-22 of a tie.
 template <bool POW2>
 __device__ __forceinline__ void scale_near(float amax, float& qscale, float& s) {
   if constexpr (POW2) {
@@ -85,7 +90,7 @@ __device__ __forceinline__ void scale_near(float amax, float& qscale, float& s) 
     const float r = near_448_over(amax);
     const bool none = !isfinite(r) || amax == 0.0f;
     qscale = none ? 1.0f : r;
-    s = none ? 1.0f : amax * (1.0f / 448.0f);
+    s = none ? 1.0f : near_over_448(amax);
   }
 }
 
@@ -323,7 +328,14 @@ __device__ __forceinline__ void emit_columns(ColumnsSmem& sm, float (&y)[8][4], 
     for (int i = 1; i < kColThreads / 32; ++i) am = fmaxf(am, sm.red[i][t]);
     float qs, s;
     scale_near<POW2>(am * fabsf(g), qs, s);
-    sm.q[t] = qs * g;
+    float k = qs * g;
+    if constexpr (!POW2) {
+      // the gain cancels: +-448 / max|y| (not where a scale of 1 stands for none, or
+      // something is not finite)
+      const float d = near_448_over(am);
+      if (isfinite(d) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) k = copysignf(d, g);
+    }
+    sm.q[t] = k;
     if (c < cols) s_t[static_cast<int64_t>(tr) * cols + c] = s;
   }
   __syncthreads();
