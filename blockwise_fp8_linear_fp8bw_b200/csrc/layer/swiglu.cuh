@@ -180,8 +180,8 @@ struct GluTileArgs {
 };
 
 // Forward: two tiles per step, half the columns apart, so that the barriers of a
-// step stand beside twice the work (16384 x 6144: 109 us, 5.6 TB/s; 113 with one
-// tile per step, in two blocks per SM).
+// step stand beside twice the work (16384 x 6144: 110 us, 5.6 TB/s; one
+// tile per step, in two blocks per SM, took 6% longer).
 constexpr int kGluFwdSlots = 6;
 using GluFwdRing = TileRing<4, kGluFwdSlots>;      // gate, up, twice
 struct GluFwdSmem {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
 // two halves): gate, up and da tiles in, a dgate and a dup tile out (16384 x 6144:
-// 168 us, 6.1 TB/s).
+// 170 us, 6.0 TB/s).
 constexpr int kGluBwdSlots = 6;
 using GluBwdRing = TileRing<3, kGluBwdSlots>;
 struct GluBwdSmem {

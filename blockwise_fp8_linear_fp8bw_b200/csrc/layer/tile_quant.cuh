@@ -144,7 +144,7 @@ struct TileEmit {
   // negative, and a maximum does not depend on the order). One slot per warp and
   // column would take 8 KB a tile, which the input ring needs more: the gated
   // product's backward pass took 230, 199 and 181 us with 3, 4 and 5 ring tiles, and
-  // 167 with the 6 that fit.
+  // 167 with the 6 that fit (170 with the present scales).
   static constexpr int kRed = kT + NOUT * kTile * kTile;         // NOUT x 128
   static constexpr int kColQ = kRed + NOUT * kTile * 4;          // NOUT x 128 floats
   static constexpr int kBytes = kColQ + NOUT * kTile * 4;
