@@ -505,3 +505,63 @@ def test_codes_feed_the_gemms():
     dw = ops.gemm_wgrad_f32(qdy_t, sdy_t, out.q_t, out.s_t)
     p, q = deq(qdy_t, sdy_t), deq(out.q_t, out.s_t)
     assert bool(((dw.double() - p @ q.t()).abs() <= 1e-3 * (p.abs() @ q.abs().t()) + 1e-30).all())
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows get what a call on them
+    alone gives (row and column groups do not look beyond their 128 rows)."""
+    torch, ops = _t(), _ops()
+    rows, cols = 140_017, 16384
+    start = 137_088                       # a multiple of 128
+    g = _gen(500)
+    x = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.randn(cols, generator=g, device="cuda")
+    assert x.numel() > 2 ** 31
+
+    def same(big, tail, first):
+        assert torch.equal(big.q[first:], tail.q) and torch.equal(big.s[:, first:], tail.s)
+        assert torch.equal(big.q_t[:, first:], tail.q_t)
+        assert torch.equal(big.s_t[first // 128:], tail.s_t)
+
+    big, tail = (ops.rmsnorm_quantize(t, gamma, t, colwise=True) for t in (x, x[start:]))
+    same(big, tail, start)
+    assert torch.equal(big.h[start:], tail.h) and torch.equal(big.rstd[start:], tail.rstd)
+    dh, dgamma = ops.rmsnorm_backward(x, big.h, big.rstd, gamma, x)
+    tail_dh, _ = ops.rmsnorm_backward(x[start:], tail.h, tail.rstd, gamma, x[start:])
+    assert torch.equal(dh[start:], tail_dh)
+    want, size = (torch.zeros(cols, dtype=torch.float64, device="cuda") for _ in range(2))
+    for i in range(0, rows, 4096):
+        t = x[i:i + 4096].double() * big.h[i:i + 4096].double() * big.rstd[i:i + 4096, None].double()
+        want += t.sum(0)
+        size += t.abs().sum(0)
+    # as R.norm_backward: every term 2 roundings, and the additions
+    assert bool(((dgamma.double() - want).abs() <= (2 + rows // 64 + 360) * R.U * size).all())
+    del big, tail, dh, tail_dh
+    same(ops.swiglu_quantize(x, colwise=True), ops.swiglu_quantize(x[start:], colwise=True), start)
+    da = x[:, :cols // 2].contiguous()
+    same(ops.swiglu_backward_quantize(da, x), ops.swiglu_backward_quantize(da[start:], x[start:]),
+         start)
+    x = x.view(-1)[:rows * 16352].view(rows, 16352)     # f = 8176: 112 past a multiple of 128
+    da = x[:, :8176].contiguous()
+    same(ops.swiglu_backward_quantize(da, x), ops.swiglu_backward_quantize(da[start:], x[start:]),
+         start)
+    ops.fp8bw_check_device_error()
+
+
+def test_newton_schulz_offsets_past_32_bits():
+    torch, ops = _t(), _ops()
+    n, k = 2 ** 17, 16400
+    g = torch.randn(n, k, generator=_gen(510), device="cuda", dtype=torch.bfloat16)
+    a, b, c = 1.5, -0.6, 0.1
+    out = ops.newton_schulz(g, steps=1, coeffs=(a, b, c))
+    norm = sum(float(g[i:i + 8192].double().square().sum()) for i in range(0, n, 8192)) ** 0.5
+    m = torch.zeros(k, k, device="cuda")
+    for i in range(0, n, 16384):
+        t = g[i:i + 16384].float() / norm
+        m += t.t() @ t
+    p = b * m + c * (m @ m)
+    for rows in (slice(0, 64), slice(n - 64, n)):
+        x = g[rows].double() / norm
+        want = a * x + x @ p.double()
+        err = float((out[rows].double() - want).norm())
+        assert err <= R.ns_tolerance(1) * float(want.norm())
