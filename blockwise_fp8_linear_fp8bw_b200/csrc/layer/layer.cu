@@ -658,15 +658,16 @@ struct NsMatrix {
   float ca, cb, cc;
 
   NsMatrix() = default;
-  NsMatrix(const fp8bw_ns_job& j, uint8_t* ws, float a, float b, float c_)
+  NsMatrix(const fp8bw_ns_job& j, uint8_t* ws, bool chained, float a, float b, float c_)
       : n(j.n), k(j.k), r(std::min(j.n, j.k)), c(std::max(j.n, j.k)), kp(ns_pitch(j.k)),
         rp(ns_pitch(std::min(j.n, j.k))), tall(j.n > j.k), w(ns_carve(ws, j.n, j.k)),
         out(j.out), ca(a), cb(b), cc(c_) {
     // A pair of steps trades 3 r^2 R flops for 3 r^3 and one launch: for R >= 3/2 r
     // where the products are long beside a launch (2 r^2 R flops of 4 G: 4 us).
     // P_1 P_0 - d_1 d_0 I has to stay below 64, its range at kQScale.
-    pairs = 2 * c >= 3 * r && static_cast<double>(r) * r * c >= 2e9 && std::fabs(ca) <= 5.0f &&
-            std::fabs(ca + cb + cc) <= 5.0f;
+    // In a chain (one launch) the products cost less than the update they save.
+    pairs = (chained || (2 * c >= 3 * r && static_cast<double>(r) * r * c >= 2e9)) &&
+            std::fabs(ca) <= 5.0f && std::fabs(ca + cb + cc) <= 5.0f;
   }
 
   // d of P - d I at a step
@@ -706,6 +707,28 @@ struct NsMatrix {
     g.diag = (shift(step) - ca) * ns::kAScale;
     return g;
   }
+  // P_1 P_0 - d_1 d_0 I of m[1] and m[2], into m[0]
+  NsGemm pair_product(int step) const {
+    NsGemm g = product(0, 1, 2, 1, ns::kQScale / (ns::kAScale * ns::kAScale),
+                       shift(step + 1) * ns::kQScale / ns::kAScale);
+    g.c2 = w.m[2];
+    g.beta2 = shift(step) * ns::kQScale / ns::kAScale;
+    return g;
+  }
+  // T = P_0 A_0 and A_1 = T P_0
+  NsGemm half_conjugate(int step) const { return product(2, 1, 0, 0, 1.0f / ns::kAScale, shift(step)); }
+  NsGemm conjugate(int step) const { return product(0, 2, 1, 2, 1.0f / ns::kAScale, shift(step)); }
+  // All of the short side's products of a step (or a pair); the index of the last.
+  int short_side(int step, bool pair, NsGemm (&g)[ns::kChainOps]) const {
+    g[0] = gram();
+    g[1] = poly(1, 0, step);
+    if (!pair) return 1;
+    g[2] = half_conjugate(step);
+    g[3] = conjugate(step);
+    g[4] = poly(2, 0, step + 1);
+    g[5] = pair_product(step);
+    return 5;
+  }
   // X <- d X + m[q] X / scale, or the result if `last`
   NsGemm update(int q, float d, float scale, bool last) {
     NsGemm g{};
@@ -729,6 +752,41 @@ struct NsMatrix {
     return g;
   }
 };
+
+// One launch: the short sides of all jobs (r <= 256) at a step, up to what multiplies
+// X; of the step and the next one, if `pair`.
+int ns_chain_launch(const NsMatrix* mat, int count, int step, bool pair, const Device& dev,
+                    cudaStream_t stream) {
+  ns::ChainMaps maps;
+  ns::ChainArgs args;
+  std::memset(&maps, 0, sizeof maps);
+  std::memset(&args, 0, sizeof args);
+  for (int i = 0; i < count; ++i) {
+    const NsMatrix& m = mat[i];
+    NsGemm g[ns::kChainOps];
+    const int last = m.short_side(step, pair, g);
+    ns::ChainJob& j = args.job[i];
+    j.r = static_cast<int>(m.r);
+    j.pitch = static_cast<int>(m.rp);
+    j.chunks = static_cast<int>(cdiv(m.c, ns::BK));
+    j.last = last;
+    j.mn = m.tall;
+    j.out = g[last].out;
+    for (int k = 0; k <= last; ++k) {
+      j.alpha[k] = g[k].alpha;
+      j.beta[k] = g[k].beta;
+      j.diag[k] = g[k].diag;
+    }
+    j.beta2 = g[last].beta2;
+    const int st = encode_operand(&maps.x[i], g[0].a, ns::BM);
+    if (st != FP8BW_OK) return st;
+  }
+  static DevicePrep prep;
+  const int st = allow_smem(prep, dev.ordinal, ns::ns_chain_kernel, ns::ChainLayout::kAlloc);
+  if (st != FP8BW_OK) return st;
+  return launched(launch_kernel(ns::ns_chain_kernel, dim3(2 * count), dim3(ns::kThreads),
+                                ns::ChainLayout::kAlloc, stream, maps, args));
+}
 
 int newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, float ca, float cb,
                   float cc, float eps, void* ws, int64_t ws_bytes, void* stream) {
@@ -763,10 +821,15 @@ int newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, 
   int64_t most = 0;
   bool any_pairs = false;
   uint8_t* p = static_cast<uint8_t*>(ws);
+  // Chains for calls of small matrices only: beside a large one they would be one
+  // more launch to wait for, where its launches have room for their tiles.
+  bool chained = true;
+  for (int i = 0; i < count; ++i)
+    chained = chained && std::min(jobs[i].n, jobs[i].k) <= ns::kChainDim;
   for (int i = 0; i < count; ++i) {
     const fp8bw_ns_job& j = jobs[i];
     if (j.n == 0 || j.k == 0) continue;
-    mat[nl] = NsMatrix(j, p, ca, cb, cc);
+    mat[nl] = NsMatrix(j, p, chained, ca, cb, cc);
     p += ns_job_bytes(j.n, j.k);
     const NsMatrix& m = mat[nl];
     in.job[nl] = ns::InJob{j.g, j.n * j.k, static_cast<int>(j.k), static_cast<int>(m.kp),
@@ -801,30 +864,27 @@ int newton_schulz(const fp8bw_ns_job* jobs, int count, int g_is_f32, int steps, 
     const bool pair = any_pairs && i + 2 <= steps &&
                       (i == 0 || (steps >= 5 && i == steps - 2));
     const bool last = i + (pair ? 2 : 1) == steps;
-    launch([&](NsMatrix& m, NsGemm* g) { return *g = m.gram(), true; });
-    launch([&](NsMatrix& m, NsGemm* g) { return *g = m.poly(1, 0, i), true; });
+    if (chained) {
+      st = ns_chain_launch(mat, nl, i, pair, dev, cs);
+    } else {
+      launch([&](NsMatrix& m, NsGemm* g) { return *g = m.gram(), true; });
+      launch([&](NsMatrix& m, NsGemm* g) { return *g = m.poly(1, 0, i), true; });
+    }
     if (pair) {
-      // matrices that take no pairs go on step by step in the same launches
-      launch([&](NsMatrix& m, NsGemm* g) {
-        *g = m.pairs ? m.product(2, 1, 0, 0, 1.0f / a, m.shift(i))          // T = P_0 A_0
-                     : m.update(1, m.shift(i), a, false);
-        return true;
-      });
-      launch([&](NsMatrix& m, NsGemm* g) {
-        *g = m.pairs ? m.product(0, 2, 1, 2, 1.0f / a, m.shift(i)) : m.gram();   // A_1 = T P_0
-        return true;
-      });
-      launch([&](NsMatrix& m, NsGemm* g) {
-        return *g = m.pairs ? m.poly(2, 0, i + 1) : m.poly(1, 0, i + 1), true;
-      });
-      launch([&](NsMatrix& m, NsGemm* g) {
-        if (!m.pairs) return false;
-        // P_1 P_0 - d_1 d_0 I
-        *g = m.product(0, 1, 2, 1, ns::kQScale / (a * a), m.shift(i + 1) * ns::kQScale / a);
-        g->c2 = m.w.m[2];
-        g->beta2 = m.shift(i) * ns::kQScale / a;
-        return true;
-      });
+      if (!chained) {
+        // matrices that take no pairs go on step by step in the same launches
+        launch([&](NsMatrix& m, NsGemm* g) {
+          *g = m.pairs ? m.half_conjugate(i) : m.update(1, m.shift(i), a, false);
+          return true;
+        });
+        launch([&](NsMatrix& m, NsGemm* g) {
+          return *g = m.pairs ? m.conjugate(i) : m.gram(), true;
+        });
+        launch([&](NsMatrix& m, NsGemm* g) {
+          return *g = m.pairs ? m.poly(2, 0, i + 1) : m.poly(1, 0, i + 1), true;
+        });
+        launch([&](NsMatrix& m, NsGemm* g) { return *g = m.pair_product(i), m.pairs; });
+      }
       launch([&](NsMatrix& m, NsGemm* g) {
         *g = m.pairs ? m.update(0, m.shift(i) * m.shift(i + 1), ns::kQScale, last)
                      : m.update(1, m.shift(i + 1), a, last);

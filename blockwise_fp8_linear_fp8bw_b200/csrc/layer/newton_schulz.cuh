@@ -18,7 +18,8 @@
 // for oblong matrices. What is lost is that A_1 is no longer made from an X that
 // exists: its rounding errors are amplified by up to a^2 = 12 for small singular
 // values. That is harmless in the first pair (A is small) and in the last (no
-// singular value is), so only those are taken so: for five steps 2 + 1 + 2.
+// singular value is), so only those are taken so: for five steps 2 + 1 + 2. (And for
+// matrices whose short side is one tile, where it saves launches: see the chain below.)
 // (Simulated against 64 bits, 256 x 1536, errors of the bf16 result: Gaussian
 // matrix 1.9e-3 step by step, 2.0e-3 with pairs; some directions 300 times the
 // rest 1.8e-3 and 2.3e-3; all steps in one pair-like run: not finite.)
@@ -193,19 +194,24 @@ __device__ __forceinline__ void store_box(uint16_t* out, int rows, int cols, int
   }
 }
 
-// v += k * (the 32 fp16 values of the lane's row of a box).
-__device__ __forceinline__ void add_scaled(float (&v)[32], uint32_t box, float k, int lane) {
+// v += k * (32 fp16 values).
+__device__ __forceinline__ void add_scaled(float (&v)[32], const uint32_t (&w)[4][4], float k) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    uint32_t w[4];
-    lds16(box_unit(box, lane, u), w);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_f16(w[e]);
-      v[8 * u + 2 * e] = fmaf(k, f.x, v[8 * u + 2 * e]);
-      v[8 * u + 2 * e + 1] = fmaf(k, f.y, v[8 * u + 2 * e + 1]);
+      const float2 f = unpack_f16(w[u][e]);
+      ffma2(v[8 * u + 2 * e], v[8 * u + 2 * e + 1], f.x, f.y, k, k);
     }
   }
+}
+
+// The same of the lane's row of a box.
+__device__ __forceinline__ void add_scaled(float (&v)[32], uint32_t box, float k, int lane) {
+  uint32_t w[4][4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) lds16(box_unit(box, lane, u), w[u]);
+  add_scaled(v, w, k);
 }
 
 // Tile `lt` of a job -> (tm, tn). Symmetric results number only the tiles that
@@ -544,6 +550,289 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty_leader0 + 8u * tb);
+    }
+    // the next launch's copies read what these stores wrote
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+  }
+
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- short sides of up to 256
+// With r <= 256 every matrix of the short side is one 256 x 256 tile, and a step's
+// products up to P (for a pair of steps, up to P_1 P_0) need nothing from outside the
+// pair of CTAs that made A: one launch does them all, a pair of CTAs per job, with the
+// matrices in shared memory (each CTA its 128 rows, 64 KB a matrix) and only what
+// multiplies X written out. All of them are symmetric, so a CTA's rows are its share
+// of both operands, in the Gram product too. Five steps are then 8 launches instead of
+// 17 (us: 256 x 768 83 instead of 100, 16 x 256 58 and 79, eight 256 x 1024 99 and 131).
+// A product takes 3.4 us: 1.1 of MMAs, 1 for the barriers, 1.4 to read TMEM, round and
+// write.
+constexpr int kChainDim = 256;
+constexpr int kChainOps = 6;            // the Gram product and up to five more
+
+struct ChainJob {
+  int r, pitch;                         // rows and row pitch of the result
+  int chunks;                           // of the Gram product's contraction
+  int last;                             // index of the last product: 1, or 5 for a pair
+  int mn;                               // X stored with the contraction outermost
+  uint16_t* out;
+  float alpha[kChainOps], beta[kChainOps], diag[kChainOps];
+  float beta2;                          // of a pair's last product
+};
+struct ChainArgs {
+  ChainJob job[kMaxJobs];
+};
+struct ChainMaps {
+  CUtensorMap x[kMaxJobs];
+};
+
+struct ChainLayout {
+  static constexpr int kMatrix = BM * kChainDim * 2;          // this CTA's rows of one
+  static constexpr int kStageBytes = BM * BK * 2;
+  static constexpr int kStages = 2 * kMatrix / kStageBytes;   // where matrices 1 and 2 go later
+  static constexpr int kBarOff = 3 * kMatrix;
+  static constexpr int kNumBars = 2 * kStages + 4;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kAlloc = kMiscOff + 16 + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
+
+// Product i = 1 .. 5 is alpha a b + beta c, of matrices
+//   P_0 = (A_0, A_0; A_0), T = (P_0, A_0; A_0), A_1 = (T, P_0; T), P_1 = (A_1, A_1; A_1),
+//   P_1 P_0 (P_0, P_1; P_0 and beta2 P_1)
+// kept as A_0, A_1 in 0, P_0 in 1, T and P_1 in 2: four bits per product. The last
+// one passes through the matrix that it does not read, 1 (of a step) or 0.
+__device__ __forceinline__ int chain_a(int i) { return (0x102100 >> (4 * i)) & 3; }
+__device__ __forceinline__ int chain_b(int i) { return (0x201000 >> (4 * i)) & 3; }
+__device__ __forceinline__ int chain_c(int i) { return (0x102000 >> (4 * i)) & 3; }
+__device__ __forceinline__ int chain_dst(int i) { return (0x020210 >> (4 * i)) & 3; }   // 5: 0
+
+// Byte offset of 16-byte unit u (8 elements) of a CTA's row of a matrix: K-major in
+// blocks of 64 columns with the 128-byte swizzle, as an operand of the MMAs.
+__device__ __forceinline__ uint32_t chain_unit(int row, int u) {
+  return static_cast<uint32_t>((u >> 3) * (BM * 128) + row * 128 + (((u ^ row) & 7) << 4));
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ns_chain_kernel(const __grid_constant__ ChainMaps maps, const __grid_constant__ ChainArgs args) {
+  using L = ChainLayout;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t ring = sbase + L::kMatrix;
+  const uint32_t bar0 = sbase + L::kBarOff;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+  const uint32_t ready_bar = bar0 + 8u * (2 * kStages + 2);   // both CTAs' rows are written
+  const uint32_t drain_bar = ready_bar + 8u;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMiscOff);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int j = static_cast<int>(blockIdx.x >> 1);
+  const ChainJob& job = args.job[j];
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar(0), 1);
+    mbar_init(tfull_bar(1), 1);
+    mbar_init(ready_bar, 2);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    prefetch_tmap(&maps.x[j]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  launch_dependents();
+  grid_dependency_wait();
+  const int chunks = job.chunks, last = job.last;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ X, for the Gram product
+    if (lane == 0) {
+      const uint32_t full_leader0 = mapa_shared(full_bar(0), 0);
+      const int row0 = static_cast<int>(rank) * BM;
+      const bool mn = job.mn != 0;
+      bool ok = true;
+      int c = 0;
+      for (; c < chunks; ++c) {
+        const int s = c % kStages;
+        if (!mbar_wait(empty_bar(s), ((c / kStages) & 1u) ^ 1u, abort_flag, kErrTimeoutTma)) {
+          ok = false;
+          break;
+        }
+        if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * L::kStageBytes);
+        const uint32_t dst = ring + s * L::kStageBytes, bar = full_leader0 + 8u * s;
+        if (mn)
+          tma_load_3d_pair(dst, &maps.x[j], bar, 0, c * BK, row0 / 64);
+        else
+          tma_load_3d_pair(dst, &maps.x[j], bar, 0, row0, 2 * c);
+      }
+      if (!ok && leader) {
+        for (int k = 0; k < kStages && k < c; ++k) {
+          const int i = c - 1 - k;
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(full_bar(i % kStages), (i / kStages) & 1u) &&
+                 globaltimer_ns() - t0 < kWaitLimitNs) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue (even CTA)
+    if (leader) {
+      const bool elected = elect_one();
+      const bool mn = job.mn != 0;
+      const uint32_t idesc = idesc_f16(2 * BM, kChainDim, mn, mn);
+      const uint64_t d0 = mn ? desc_mnmajor_sw128(ring, 64 * BK * 2) : desc_kmajor_sw128(ring);
+      const uint64_t ks = mn ? (16 * 128) >> 4 : 32 >> 4;
+      const uint64_t kh = (mn ? 4 * 16 * 128 : L::kStageBytes / 2) >> 4;
+      bool ok = true;
+      for (int c = 0; c < chunks; ++c) {
+        const int s = c % kStages;
+        if (!mbar_wait(full_bar(s), (c / kStages) & 1u, abort_flag, kErrTimeoutMma)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t dd = d0 + (static_cast<uint64_t>(s * L::kStageBytes) >> 4);
+        if (elected) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t dk = dd + (kk >> 2) * kh + (kk & 3) * ks;
+            mma_f16_pair(tmem_base, dk, dk, idesc, c > 0 || kk > 0 ? 1u : 0u);
+          }
+          mma_commit_pair(empty_bar(s), 0x3);
+        }
+        __syncwarp();
+      }
+      if (ok && elected) mma_commit_pair(tfull_bar(0), 0x3);
+      __syncwarp();
+      const uint32_t idesc_k = idesc_f16(2 * BM, kChainDim, false, false);
+      const int ksteps = (job.r + 15) / 16;
+      for (int i = 1; ok && i <= last; ++i) {
+        if (!mbar_wait(ready_bar, (i - 1) & 1u, abort_flag, kErrTimeoutMma)) {
+          ok = false;
+          break;
+        }
+        // the other CTA's rows were written by its threads
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        tc_fence_after();
+        const uint64_t ad = desc_kmajor_sw128(sbase + chain_a(i) * L::kMatrix);
+        const uint64_t bd = desc_kmajor_sw128(sbase + chain_b(i) * L::kMatrix);
+        if (elected) {
+          for (int kk = 0; kk < ksteps; ++kk) {
+            const uint64_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+            mma_f16_pair(tmem_base + (i & 1) * kChainDim, ad + off, bd + off, idesc_k,
+                         kk > 0 ? 1u : 0u);
+          }
+          mma_commit_pair(tfull_bar(i & 1), 0x3);
+        }
+        __syncwarp();
+      }
+      if (!ok && elected) {
+        mma_commit_pair(drain_bar, 0x1);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kFirstEpiWarp) {
+    // ------------------------------------------------------------ epilogues
+    const int q = warp & 3, hh = (warp - kFirstEpiWarp) >> 2;
+    const int row = q * 32 + lane, grow = static_cast<int>(rank) * BM + row;
+    const bool live = grow < job.r;
+    const uint32_t ready_leader = mapa_shared(ready_bar, 0);
+    for (int i = 0; i <= last; ++i) {
+      // (every wait ends; after an expired one all warps of the CTA go on to the
+      // barriers below)
+      const bool ok = mbar_wait(tfull_bar(i & 1), (i >> 1) & 1u, abort_flag, kErrTimeoutEpi);
+      if (__all_sync(0xFFFFFFFFu, ok)) {
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>((i & 1) * kChainDim + hh * 128);
+        const uint32_t cm = sbase + chain_c(i) * L::kMatrix;
+        const uint32_t dm = sbase + chain_dst(i) * L::kMatrix;
+        const float alpha = job.alpha[i], beta = job.beta[i];
+        const float diag = live ? job.diag[i] : 0.0f;      // rows past r stay zero
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t acc[32];
+          tmem_ld32(taddr + g * 32, acc);
+          const int u0 = hh * 16 + g * 4, col0 = u0 * 8;
+          uint32_t w[4][4], w2[4][4];
+          if (i > 0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) lds16(cm + chain_unit(row, u0 + u), w[u]);
+          }
+          if (i == kChainOps - 1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              lds16(sbase + 2 * L::kMatrix + chain_unit(row, u0 + u), w2[u]);
+          }
+          tmem_wait_ld();
+          tmem_regs_ready(acc);
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            fmul2(v[e], v[e + 1], __uint_as_float(acc[e]), __uint_as_float(acc[e + 1]), alpha, alpha);
+          if (i == kChainOps - 1) add_scaled(v, w2, job.beta2);
+          if (i > 0) add_scaled(v, w, beta);
+          if (grow >= col0 && grow < col0 + 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] -= col0 + e == grow ? diag : 0.0f;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack_f16(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
+            sts16(dm + chain_unit(row, u0 + u), o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if (i < last) fence_proxy_async_smem();
+      tc_fence_before();
+      asm volatile("bar.sync 1, %0;" ::"n"(kNumEpiWarps * 32) : "memory");
+      if (i == last) {
+        // the result, a row of up to 512 bytes per warp and instruction
+        const uint32_t dm = sbase + chain_dst(i) * L::kMatrix;
+        if (8 * lane < job.pitch) {
+          for (int rr = warp - kFirstEpiWarp; rr < min(BM, job.r - static_cast<int>(rank) * BM);
+               rr += kNumEpiWarps) {
+            uint32_t o[4];
+            lds16(dm + chain_unit(rr, lane), o);
+            *reinterpret_cast<uint4*>(
+                job.out + static_cast<int64_t>(static_cast<int>(rank) * BM + rr) * job.pitch +
+                8 * lane) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        break;
+      }
+      if (warp == kFirstEpiWarp && lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ready_leader)
+                     : "memory");
     }
     // the next launch's copies read what these stores wrote
     asm volatile("fence.proxy.async.global;" ::: "memory");

@@ -236,7 +236,8 @@ def test_non_finite_values_stay_in_their_row(bad):
 
 NS_SHAPES = [["16x16"], ["16x256", "256x16"], ["48x400", "272x272"], ["256x768"],
              ["768x256", "512x512", "16x2048"], ["1040x1296"], ["1296x1040"],
-             ["640x640"] * 9]
+             ["640x640"] * 9, ["256x256"], ["112x1408", "2064x192", "16x64", "64x16", "240x272",
+                               "256x3088", "1040x256", "128x128"]]
 
 
 @pytest.mark.parametrize("shapes", NS_SHAPES, ids=lambda s: "+".join(s)[:40])
@@ -263,7 +264,8 @@ def test_newton_schulz(shapes, steps, f32):
 
 
 @pytest.mark.parametrize("shapes", [["1040x2064"], ["2320x1040", "512x272", "1040x1040"],
-                                    ["1136x1712", "16x48", "1712x1136"]],
+                                    ["1136x1712", "16x48", "1712x1136"],
+                                    ["208x656", "144x144", "3088x256"]],
                          ids=lambda s: "+".join(s))
 @pytest.mark.parametrize("steps", [2, 3, 5, 6, 7])
 def test_newton_schulz_pairs_of_steps(shapes, steps):
@@ -280,10 +282,11 @@ def test_newton_schulz_pairs_of_steps(shapes, steps):
     assert all(torch.equal(a, b) for a, b in zip(outs, ops.newton_schulz_batch(gs, steps=steps)))
 
 
-def test_newton_schulz_pairs_with_other_coefficients_and_spectra():
+@pytest.mark.parametrize("short", [1040, 240])
+def test_newton_schulz_pairs_with_other_coefficients_and_spectra(short):
     torch, ops = _t(), _ops()
-    g = _normal((1040, 2064), 260, 1e-3, torch.float32)
-    u = torch.linalg.qr(_normal((1040, 4), 261, 1.0, torch.float32))[0]
+    g = _normal((short, 2064), 260, 1e-3, torch.float32)
+    u = torch.linalg.qr(_normal((short, 4), 261, 1.0, torch.float32))[0]
     v = torch.linalg.qr(_normal((2064, 4), 262, 1.0, torch.float32))[0]
     low = g + 20.0 * u @ v.t()               # four directions some 250 times the rest
     for m, coeffs in ((low, (3.4445, -4.7750, 2.0315)), (g, (1.5, -0.5, 0.0)),
