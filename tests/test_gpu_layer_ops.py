@@ -336,6 +336,23 @@ def test_newton_schulz_singular_values_and_extremes():
     assert float((got.double() - ref).norm()) <= R.ns_tolerance(3) * float(ref.norm())
 
 
+@pytest.mark.parametrize("shapes", [((64, 400), (256, 256)), ((400, 640), (528, 272))])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_newton_schulz_non_finite_matrix_beside_others(shapes, bad):
+    """A matrix with a value that is not finite comes out not finite; the others of
+    the call, and a matrix of zeros among them, do not notice."""
+    torch, ops = _t(), _ops()
+    a, b = (_normal(s, 310 + i, 1e-3, torch.float32) for i, s in enumerate(shapes))
+    z = torch.zeros(48, 80, device="cuda")
+    want = ops.newton_schulz_batch([a, z, b])
+    broken = a.clone()
+    broken[3, 5] = bad
+    got = ops.newton_schulz_batch([broken, z, b])
+    ops.fp8bw_check_device_error()
+    assert not bool(torch.isfinite(got[0].float()).all())
+    assert not bool(got[1].any()) and torch.equal(got[2], want[2])
+
+
 def test_no_rows_and_empty_matrices():
     torch, ops = _t(), _ops()
     x = torch.empty(0, 256, device="cuda", dtype=torch.bfloat16)
