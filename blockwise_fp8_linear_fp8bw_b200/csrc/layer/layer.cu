@@ -524,9 +524,10 @@ int64_t ns_tiles(const NsGemm& g, int bn) {
 // The longest cluster's time under the kernel's tile order, in chunks of a
 // 256-wide tile. A chunk costs what its two operand boxes cost the TMA unit (120
 // cycles each, and 64 bytes a cycle): 1260 cycles with 256 columns (32 + 32 KB),
-// 1010 with 128 (32 + 16 KB). A tile also costs about a chunk of pipeline fill.
+// 1010 with 128 (32 + 16 KB), 880 with 64 (32 + 8 KB). A tile also costs about a
+// chunk of pipeline fill.
 double ns_makespan(const NsGemm* g, int count, int bn, int clusters) {
-  const double chunk = bn == 256 ? 1.0 : 0.8;
+  const double chunk = bn == 256 ? 1.0 : bn == 128 ? 0.8 : 0.7;
   int64_t total = 0;
   double sum = 0.0;
   for (int i = 0; i < count; ++i) {
@@ -599,13 +600,22 @@ int ns_clusters(const Device& dev, int* clusters) {
 int ns_launch(NsGemm* g, int count, const Device& dev, cudaStream_t stream) {
   // long contractions first (see the kernel's tile order)
   std::stable_sort(g, g + count, [](const NsGemm& x, const NsGemm& y) { return x.kc > y.kc; });
-  int c256 = 0, c128 = 0;
+  int c256 = 0, c128 = 0, c64 = 0;
   int st = ns_clusters<256>(dev, &c256);
   if (st == FP8BW_OK) st = ns_clusters<128>(dev, &c128);
+  if (st == FP8BW_OK) st = ns_clusters<64>(dev, &c64);
   if (st != FP8BW_OK) return st;
-  // 128-wide tiles where they spread the work better over the clusters
-  const int bn =
-      ns_makespan(g, count, 128, c128) < 0.97 * ns_makespan(g, count, 256, c256) ? 128 : 256;
+  // Narrower tiles where they spread the work better over the clusters (five steps,
+  // us, with tiles of 64 and without: 512 x 512 111 and 125, 1024 x 1024 139 and 153,
+  // 1024 x 4096 199 and 226)
+  int bn = 256, clusters = c256;
+  double best = ns_makespan(g, count, 256, c256);
+  const double w128 = ns_makespan(g, count, 128, c128);
+  if (w128 < 0.97 * best) bn = 128, clusters = c128, best = w128;
+  // (64: not with MN-major B, whose 128-byte rows are 64 columns of a CTA)
+  bool narrow = true;
+  for (int i = 0; i < count; ++i) narrow = narrow && !g[i].b.mn;
+  if (narrow && ns_makespan(g, count, 64, c64) < 0.97 * best) bn = 64, clusters = c64;
   ns::Maps maps;
   ns::Args args;
   std::memset(&maps, 0, sizeof maps);
@@ -639,12 +649,14 @@ int ns_launch(NsGemm* g, int count, const Device& dev, cudaStream_t stream) {
     if (st != FP8BW_OK) return st;
   }
   args.count = count;
-  const int clusters = static_cast<int>(std::min<int64_t>(bn == 256 ? c256 : c128, tiles));
-  const dim3 grid(2 * clusters), block(ns::kThreads);
+  const dim3 grid(2 * static_cast<unsigned>(std::min<int64_t>(clusters, tiles))), block(ns::kThreads);
   if (bn == 256)
     return launched(launch_kernel(ns::ns_gemm_kernel<256>, grid, block, ns::Layout<256>::kAlloc,
                                   stream, maps, args));
-  return launched(launch_kernel(ns::ns_gemm_kernel<128>, grid, block, ns::Layout<128>::kAlloc,
+  if (bn == 128)
+    return launched(launch_kernel(ns::ns_gemm_kernel<128>, grid, block, ns::Layout<128>::kAlloc,
+                                  stream, maps, args));
+  return launched(launch_kernel(ns::ns_gemm_kernel<64>, grid, block, ns::Layout<64>::kAlloc,
                                 stream, maps, args));
 }
 
