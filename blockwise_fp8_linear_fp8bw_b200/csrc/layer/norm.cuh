@@ -268,9 +268,12 @@ __global__ void __launch_bounds__(V * R == 1 ? 1024 : 512)
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float k = __shfl_sync(0xFFFFFFFFu, f, (lane & 16) | (i * kShare));
-    uint2 w;
-    w.x = encode4(y[i][0], y[i][1], y[i][2], y[i][3], k);
-    w.y = encode4(y[i][4], y[i][5], y[i][6], y[i][7], k);
+    // (a padding row is zero whatever its factor is: without eps its rstd is infinite)
+    uint2 w = make_uint2(0u, 0u);
+    if (live(i)) {
+      w.x = encode4(y[i][0], y[i][1], y[i][2], y[i][3], k);
+      w.y = encode4(y[i][4], y[i][5], y[i][6], y[i][7], k);
+    }
     if (row0 + i % R < a.rows_pad && has(i)) *reinterpret_cast<uint2*>(a.q + at(i)) = w;
   }
 }
