@@ -240,41 +240,90 @@ __global__ void __launch_bounds__(V * R == 1 ? 1024 : 512)
     if (live(r) && t == 0 && a.rstd != nullptr) a.rstd[row0 + r] = rstd[r];
     if (mine % R == r) my_rstd = rstd[r];
   }
+  const int64_t first = (t & ~15) + mine / R * tpr;   // first chunk of this lane's group
+  const bool group = FULL || first < chunks;
 
+  // (h gamma) rstd, the order above, may leave fp32's range where (h rstd) gamma does
+  // not. What is outside of [2^-100, 2^120] on the way is done over below, from h once
+  // more and in the formula's order. (Zeros only where rstd could bring a product
+  // below 2^-150 back.)
+  auto outside = [](float v, float rs) {
+    return !(v >= 0x1p-100f && v <= 0x1p120f) && !(v == 0.0f && rs <= 1024.0f);
+  };
+  uint32_t low = 0u;                           // items with such a value of y
   if (a.y != nullptr) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!live(i) || !has(i)) continue;
       uint32_t w[4];
 #pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (outside(fabsf(y[i][j]), rstd[i % R])) low |= 1u << i;
+#pragma unroll
       for (int j = 0; j < 4; ++j)
         w[j] = pack_bf16(y[i][2 * j] * rstd[i % R], y[i][2 * j + 1] * rstd[i % R]);
       *reinterpret_cast<uint4*>(a.y + at(i)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  if (a.q == nullptr) return;
-  float qs, s;
-  scale_near<POW2>(m[0] * my_rstd, qs, s);
-  float f = qs * my_rstd;
-  if constexpr (!POW2) {
-    // rstd cancels: 448 / max|h gamma|, three roundings fewer (not where a scale of
-    // 1 stands for none, or something is not finite)
-    const float d = near_448_over(m[0]);
-    if (isfinite(d) && isfinite(my_rstd) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) f = d;
-  }
-  const int64_t first = (t & ~15) + mine / R * tpr;   // first chunk of this lane's group
-  if ((lane & (kShare - 1)) == 0 && row0 + mine % R < a.rows_pad && (FULL || first < chunks))
-    a.s[(first >> 4) * a.rows_pad + row0 + mine % R] = s;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float k = __shfl_sync(0xFFFFFFFFu, f, (lane & 16) | (i * kShare));
-    // (a padding row is zero whatever its factor is: without eps its rstd is infinite)
-    uint2 w = make_uint2(0u, 0u);
-    if (live(i)) {
-      w.x = encode4(y[i][0], y[i][1], y[i][2], y[i][3], k);
-      w.y = encode4(y[i][4], y[i][5], y[i][6], y[i][7], k);
+  bool odd = false;                            // a group's codes
+  if (a.q != nullptr) {
+    const float top = m[0] * my_rstd;
+    odd = group && row0 + mine % R < a.rows && (outside(m[0], my_rstd) || !(top <= 0x1p120f));
+    float qs, s;
+    scale_near<POW2>(top, qs, s);
+    float f = qs * my_rstd;
+    if constexpr (!POW2) {
+      // rstd cancels: 448 / max|h gamma|, three roundings fewer (not where a scale of
+      // 1 stands for none)
+      const float d = near_448_over(m[0]);
+      if (isfinite(d) && !(qs == 1.0f && s == 1.0f)) f = d;
     }
-    if (row0 + i % R < a.rows_pad && has(i)) *reinterpret_cast<uint2*>(a.q + at(i)) = w;
+    if ((lane & (kShare - 1)) == 0 && row0 + mine % R < a.rows_pad && group && !odd)
+      a.s[(first >> 4) * a.rows_pad + row0 + mine % R] = s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float k = __shfl_sync(0xFFFFFFFFu, f, (lane & 16) | (i * kShare));
+      // (a padding row is zero whatever its factor is: without eps its rstd is infinite)
+      uint2 w = make_uint2(0u, 0u);
+      if (live(i)) {
+        w.x = encode4(y[i][0], y[i][1], y[i][2], y[i][3], k);
+        w.y = encode4(y[i][4], y[i][5], y[i][6], y[i][7], k);
+      }
+      if (row0 + i % R < a.rows_pad && has(i)) *reinterpret_cast<uint2*>(a.q + at(i)) = w;
+    }
+  }
+  if (!__any_sync(0xFFFFFFFFu, odd || low != 0u)) return;
+  // (each thread over what it wrote itself)
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) {
+    const int from = (lane & 16) | (i * kShare);
+    const float rs = __shfl_sync(0xFFFFFFFFu, my_rstd, from);
+    const bool codes = __shfl_sync(0xFFFFFFFFu, odd, from) != 0 && has(i);
+    float v[8], most = 0.0f;
+    if (codes || (low >> i & 1u)) {
+      float g[8];
+      uint4 w = ld16_again(a.x + at(i));
+      if (a.residual != nullptr) w = add_bf16x8(w, ld16_again(a.residual + at(i)));
+      unpack8(w, v);
+      load_gamma8(a.gamma, a.gamma_f32, 8 * static_cast<int64_t>(t + i / R * tpr), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = __fmul_rn(__fmul_rn(v[j], rs), g[j]);
+        most = max3_abs(most, v[j], v[j]);
+      }
+      if (low >> i & 1u)
+        *reinterpret_cast<uint4*>(a.y + at(i)) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                       pack_bf16(v[6], v[7]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    if (!codes) continue;
+    float qs, s;
+    scale_near<POW2>(most, qs, s);
+    *reinterpret_cast<uint2*>(a.q + at(i)) =
+        make_uint2(encode4(v[0], v[1], v[2], v[3], qs), encode4(v[4], v[5], v[6], v[7], qs));
+    if ((lane & 15) == 0) a.s[((t + i / R * tpr) >> 4) * a.rows_pad + row0 + i % R] = s;
   }
 }
 
@@ -337,6 +386,7 @@ __global__ void __launch_bounds__(kColThreads, 4) norm_col_kernel(const NormColA
     }
   }
   emit_columns<POW2>(sm, y, m, tr, tc, a.rows_pad, a.cols, a.q_t, a.s_t,
+                     static_cast<int>(min(max(a.rows - r0, int64_t(0)), int64_t(8))),
                      [&](int64_t c) { return load_gamma(a.gamma, a.gamma_f32, c); });
 }
 

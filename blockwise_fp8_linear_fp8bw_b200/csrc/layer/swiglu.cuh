@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kColThreads) swiglu_few_kernel(const GluFewArg
       for (int j = 0; j < 4; ++j) m[j] = max3_abs(m[j], y[p - 1][j], y[p][j]);
     }
   }
-  emit_columns<POW2>(sm, y, m, tr, tc, a.out.rows, a.out.cols, a.out.q_t, a.out.s_t,
-                     [](int64_t) { return 1.0f; });
+  emit_columns<POW2>(sm, y, m, tr, tc, a.out.rows, a.out.cols, a.out.q_t, a.out.s_t, 8,
+                     NoGain());
 }
 
 // ---------------------------------------------------------------- 128x128 tiles

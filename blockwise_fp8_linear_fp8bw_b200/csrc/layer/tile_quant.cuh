@@ -11,6 +11,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "../common.cuh"
 
 namespace fp8bw {
@@ -305,45 +307,82 @@ constexpr int kColThreads = 256;
 struct ColumnsSmem {
   float red[kColThreads / 32][kColTile];
   float q[kColTile];
+  float q2[kColTile];
   __align__(16) uint8_t t[kColTile * kTile];
 };
 
+// Gain of a product that has none.
+struct NoGain {
+  __device__ __forceinline__ float operator()(int64_t) const { return 1.0f; }
+};
+
 // Of y times gain(column), from the thread's column maxima m of |y|; entries outside
-// the tensor must be zero.
+// the tensor must be zero, and are in the codes whatever the gain: `live` of the
+// thread's rows are inside.
 template <bool POW2, typename Gain>
 __device__ __forceinline__ void emit_columns(ColumnsSmem& sm, float (&y)[8][4], float (&m)[4],
                                              int tr, int tc, int64_t rows_pad, int64_t cols,
-                                             uint8_t* q_t, float* s_t, Gain&& gain) {
+                                             uint8_t* q_t, float* s_t, int live, Gain&& gain) {
+  constexpr bool kGain = !std::is_same<std::decay_t<Gain>, NoGain>::value;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, rb = t >> 4, cb = t & 15;
 #pragma unroll
   for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
   if (lane < 16)
     *reinterpret_cast<float4*>(&sm.red[warp][cb * 4]) = make_float4(m[0], m[1], m[2], m[3]);
   __syncthreads();
+  bool odd = false;
   if (t < kColTile) {
     const int64_t c = static_cast<int64_t>(tc) * kColTile + t;
-    const float g = c < cols ? gain(c) : 0.0f;
     float am = sm.red[0][t];
 #pragma unroll
     for (int i = 1; i < kColThreads / 32; ++i) am = fmaxf(am, sm.red[i][t]);
     float qs, s;
-    scale_near<POW2>(am * fabsf(g), qs, s);
-    float k = qs * g;
-    if constexpr (!POW2) {
-      // the gain cancels: +-448 / max|y| (not where a scale of 1 stands for none, or
-      // something is not finite)
-      const float d = near_448_over(am);
-      if (isfinite(d) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) k = copysignf(d, g);
+    if constexpr (kGain) {
+      const float g = c < cols ? gain(c) : 0.0f;
+      const float top = am * fabsf(g);
+      scale_near<POW2>(top, qs, s);
+      float k = qs * g;
+      if constexpr (!POW2) {
+        // the gain cancels: +-448 / max|y| (not where a scale of 1 stands for none, or
+        // something is not finite)
+        const float d = near_448_over(am);
+        if (isfinite(d) && qs > 0.0f && !(qs == 1.0f && s == 1.0f)) k = copysignf(d, g);
+      }
+      // where one factor for gain and scale may leave fp32's range: one after the other
+      odd = !(am >= 0x1p-100f && top <= 0x1p120f) && am != 0.0f;
+      sm.q[t] = odd ? g : k;
+      sm.q2[t] = odd ? qs : 1.0f;
+    } else {
+      scale_near<POW2>(am, qs, s);
+      sm.q[t] = qs;
     }
-    sm.q[t] = k;
     if (c < cols) s_t[static_cast<int64_t>(tr) * cols + c] = s;
   }
-  __syncthreads();
+  bool twice = false;
+  if constexpr (kGain) twice = __syncthreads_or(odd) != 0;
+  else __syncthreads();
   const float4 k = *reinterpret_cast<const float4*>(&sm.q[cb * 4]);
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     fmul2(y[p][0], y[p][1], y[p][0], y[p][1], k.x, k.y);
     fmul2(y[p][2], y[p][3], y[p][2], y[p][3], k.z, k.w);
+  }
+  if constexpr (kGain) {
+    if (twice) {
+      const float4 k2 = *reinterpret_cast<const float4*>(&sm.q2[cb * 4]);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        fmul2(y[p][0], y[p][1], y[p][0], y[p][1], k2.x, k2.y);
+        fmul2(y[p][2], y[p][3], y[p][2], y[p][3], k2.z, k2.w);
+      }
+    }
+    if (live < 8) {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        if (p < live) continue;
+        y[p][0] = y[p][1] = y[p][2] = y[p][3] = 0.0f;
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)

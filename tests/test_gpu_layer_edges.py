@@ -77,3 +77,113 @@ def test_block_without_eps(tokens, pow2):
         got.append((y.detach(), h.detach(), xx.grad, *(p.grad for p in m.parameters())))
     assert all(bool(torch.isfinite(t.float()).all()) for t in got[0])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def _check_norm(x, gamma, r, eps, pow2, rows):
+    """Codes both ways and the bf16 output against the 64-bit norm; -> the codes."""
+    torch, ops = _t(), _ops()
+    _, _, v, err = R.norm(x, r, gamma, eps)
+    out = ops.rmsnorm_quantize(x, gamma, r, eps, colwise=True, pow2=pow2)
+    row = ops.rmsnorm_quantize(x, gamma, r, eps, pow2=pow2)
+    assert torch.equal(out.q, row.q) and torch.equal(out.s, row.s)
+    R.check_codes(out.q, out.s, v, err, 1, pow2, rows)
+    R.check_codes(out.q_t, out.s_t, v, err, 0, pow2, rows)
+    zero = v == 0
+    assert not bool(_values(out.q[:rows])[zero].ne(0).any())
+    assert not bool(_values(out.q_t[:, :rows]).t()[zero].ne(0).any())
+    _padding_is_zero(out, rows)
+    y, _, _ = ops.rmsnorm(x, gamma, r, eps)
+    assert bool(((y.double() - v).abs() <= err + 2.0 ** -8 * v.abs() + 2.0 ** -134).all())
+    ops.fp8bw_check_device_error()
+    return out
+
+
+@pytest.mark.parametrize("rows,cols", RAGGED)
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_nearly_empty_groups(rows, cols, pow2, residual):
+    """A group, a row and a column of zeros and one value of 1e-37: the factor of the
+    codes is beyond fp32's range, the codes are not."""
+    torch = _t()
+    x = _normal((rows, cols), 20)
+    gamma = torch.full((cols,), 4.0, device="cuda")
+    x[:, 3] = 0                                   # a column
+    x[rows // 2, 3] = 1e-37
+    if cols > 128:
+        x[rows // 3, 128:256] = 0                 # a 1x128 group
+        x[rows // 3, 130] = -1e-37
+    if rows > 2:
+        x[rows - 1] = 0                           # a row
+        x[rows - 1, cols - 1] = 1e-37
+    r = torch.zeros_like(x) if residual else None
+    _check_norm(x, gamma, r, 1e-6, pow2, rows)
+
+
+@pytest.mark.parametrize("rows,cols", RAGGED)
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("size,weight", [(2.0 ** 40, 2.0 ** 100), (2.0 ** -40, 2.0 ** -100),
+                                         (2.0 ** -40, 2.0 ** 80), (2.0 ** 40, 2.0 ** -80)])
+def test_norm_in_the_formulas_order(rows, cols, pow2, size, weight):
+    """h rstd is of order one whatever h, so (h rstd) gamma is in fp32's range where
+    h gamma is not (without eps). Every third column has such a weight."""
+    torch = _t()
+    x = _normal((rows, cols), 30, size)
+    gamma = 1 + _normal((cols,), 31, 0.2, torch.float32)
+    gamma[::3] *= weight
+    _check_norm(x, gamma, None, 0.0, pow2, rows)
+    gamma = (1 + _normal((cols,), 32, 0.2, torch.float32)) * weight
+    _check_norm(x, gamma, None, 0.0, pow2, rows)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 16), (17, 2048), (149, 8192), (10005, 144), (1237, 1040)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_norm_weight_that_is_not_finite(rows, cols, bad, pow2):
+    """It spoils its own column; the padding rows' codes stay zero."""
+    torch, ops = _t(), _ops()
+    x = _normal((rows, cols), 40)
+    gamma = torch.ones(cols, device="cuda")
+    gamma[5] = bad
+    out = ops.rmsnorm_quantize(x, gamma, None, colwise=True, pow2=pow2)
+    _padding_is_zero(out, rows)
+    want = ops.rmsnorm_quantize(x, torch.ones_like(gamma), None, colwise=True, pow2=pow2)
+    keep = [i for i in range(cols) if i != 5]
+    assert torch.equal(out.q_t[keep], want.q_t[keep])
+    assert torch.equal(out.s_t[:, keep], want.s_t[:, keep])
+    assert torch.equal(out.rstd, want.rstd)
+    v = _values(out.q_t)[5, :rows] * out.s_t[:, 5].repeat_interleave(128)[:rows]
+    if pow2 and bad > 0:
+        # the power-of-two rule gives a group with an infinity the scale 1, and
+        # infinity times 1 saturates at E4M3's largest value
+        assert bool((v.abs() == 448).all())
+    else:
+        assert not bool(torch.isfinite(v).any())
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_odd_groups_leave_their_neighbours_alone(pow2):
+    """A row with values at the end of the range does not change what the rows and
+    columns beside it get."""
+    torch, ops = _t(), _ops()
+    for rows, cols in RAGGED[1:]:
+        x = _normal((rows, cols), 50)
+        gamma = 1 + _normal((cols,), 51, 0.2)
+        want = ops.rmsnorm_quantize(x, gamma, colwise=True, pow2=pow2)
+        y = x.clone()
+        y[5] = 0
+        y[5, 7] = 1e-37
+        got = ops.rmsnorm_quantize(y, gamma, colwise=True, pow2=pow2)
+        keep = [i for i in range(rows) if i != 5]
+        assert torch.equal(got.q[keep], want.q[keep])
+        assert torch.equal(got.s[:, keep], want.s[:, keep])
+        y = x.clone()
+        y[:, 7] = 0
+        g = gamma.clone()
+        g[7] = 4.0
+        y[rows // 2, 7] = 1e-37                   # (rstd is the same with or without it)
+        z = y.clone()
+        z[:, 7] = 0
+        got, want = (ops.rmsnorm_quantize(t, g, colwise=True, pow2=pow2) for t in (y, z))
+        keep = [i for i in range(cols) if i != 7]
+        assert torch.equal(got.q_t[keep], want.q_t[keep])
+        assert torch.equal(got.s_t[:, keep], want.s_t[:, keep])
