@@ -498,6 +498,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (cp2 != nullptr) add_scaled(v, slot + L::kBoxBytes, beta2, lane);
           add_scaled(v, slot, beta, lane);
+          // a mirror image goes into rows of the second box that other lanes read C2 from
+          if (cp2 != nullptr && mirror) __syncwarp();
         }
         if (y0 == x0 + gi * 32) {      // a box on the diagonal
 #pragma unroll
