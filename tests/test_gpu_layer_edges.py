@@ -187,3 +187,61 @@ def test_odd_groups_leave_their_neighbours_alone(pow2):
         keep = [i for i in range(cols) if i != 7]
         assert torch.equal(got.q_t[keep], want.q_t[keep])
         assert torch.equal(got.s_t[:, keep], want.s_t[:, keep])
+
+
+def _every_gate(low, high):
+    """Every bf16 value from low to high."""
+    torch = _t()
+    v = torch.arange(1 << 16, device="cuda", dtype=torch.int32).to(torch.int16)
+    v = v.view(torch.bfloat16)
+    v = v[torch.isfinite(v.float()) & (v >= low) & (v <= high)]
+    return v
+
+
+@pytest.mark.parametrize("low,high", [(-80.0, -20.0), (-20.0, -2.0 ** -4), (2.0 ** -4, 100.0)])
+def test_sigmoid_of_every_gate(low, high):
+    """The scale of a group shows its largest value without a rounding to few bits.
+    In units of u = 2^-24 relative: the approximate exponential 4 (2^-22), its argument's
+    remainder to first order 1 and, at 80, 1.3 of second order, 1 + e 1, the approximate
+    reciprocal 2, two products 1 each, the quotient 1."""
+    torch, ops = _t(), _ops()
+    gate = _every_gate(low, high)
+    gu = torch.ones(gate.numel(), 256, device="cuda", dtype=torch.bfloat16)
+    gu[:, :128] = gate[:, None]
+    want = gate.double().abs() * torch.sigmoid(gate.double()) / 448.0
+    for colwise in (False, True):
+        got = ops.swiglu_quantize(gu, colwise=colwise).s[0, :gate.numel()].double()
+        assert bool(((got - want).abs() <= 12.4 * R.U * want).all())
+    # and of the gradient: dup = da gate sigmoid(gate), a product less
+    da = torch.ones(gate.numel(), 128, device="cuda", dtype=torch.bfloat16)
+    got = ops.swiglu_backward_quantize(da, gu).s[1, :gate.numel()].double()
+    assert bool(((got - want).abs() <= 12.4 * R.U * want).all())
+
+
+def test_gates_that_are_not_finite():
+    """gate = inf: a is infinite, and its group's scale; -inf and NaN: NaN codes, and the
+    rest of the group as without them."""
+    torch, ops = _t(), _ops()
+    inf = float("inf")
+    gu = _normal((48, 512), 60)
+    gu[7, 256 + 9] = 1.0
+    for rows in (48, 4000):                       # both forms
+        x = gu.repeat(rows // 48 + 1, 1)[:rows]
+        ref = ops.swiglu_quantize(x, colwise=True)
+        for bad, s in ((inf, inf), (-inf, None), (float("nan"), None)):
+            y = x.clone()
+            y[7, 9] = bad
+            out = ops.swiglu_quantize(y, colwise=True)
+            assert bool(torch.isnan(_values(out.q)[7, 9]))
+            assert bool(torch.isnan(_values(out.q_t)[9, 7]))
+            if s is not None:
+                assert float(out.s[0, 7]) == inf and float(out.s_t[0, 9]) == inf
+            q, keep = out.q.clone(), ref.q.clone()
+            q[7, :128], keep[7, :128] = 0, 0
+            assert torch.equal(q, keep)
+            if s is None:
+                v = _values(out.q)[7, :128] * out.s[0, 7]
+                w = _values(ref.q)[7, :128] * ref.s[0, 7]
+                v[9] = w[9]
+                # (another largest value, another rounding)
+                assert bool(((v - w).abs() <= 2.0 ** -4 * w.abs() + ref.s[0, 7] * 2.0 ** -9).all())
