@@ -64,9 +64,11 @@ __device__ __forceinline__ float max3_abs(float m, float a, float b) {
   return r;
 }
 
-// 448 / amax within an ulp: the approximate reciprocal (of amax / 16, so that no
-// finite amax has a subnormal one) and a correction by what the product leaves of
-// 448. 0 for infinity, infinite or NaN where the quotient is.
+// 448 / amax: the approximate reciprocal (of amax / 16, so that no finite amax has a
+// subnormal one) and a correction by what the product leaves of 448. It equals the
+// correctly rounded quotient for every positive fp32 amax (compared with IEEE
+// division over all of them), as near_over_448 does where 448 / amax is finite.
+// 0 for infinity, infinite or NaN where the quotient is.
 __device__ __forceinline__ float near_448_over(float amax) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * 0.0625f));
@@ -80,10 +82,8 @@ __device__ __forceinline__ float near_over_448(float amax) {
   return isfinite(amax) ? fmaf(fmaf(-q, 448.0f, amax), 1.0f / 448.0f, q) : q;
 }
 
-// scale_of for the fused kernels: the quotients are within an ulp instead of
-// correctly rounded (two IEEE divisions cost some 40 instructions and their
-// latency, in every step). amax still encodes as 448, and other codes differ only
-// for values within 2^-22 of a tie.
+// scale_of for the fused kernels: the same scales without IEEE divisions (some 40
+// instructions and their latency, in every step).
 template <bool POW2>
 __device__ __forceinline__ void scale_near(float amax, float& qscale, float& s) {
   if constexpr (POW2) {

@@ -245,3 +245,61 @@ def test_gates_that_are_not_finite():
                 v[9] = w[9]
                 # (another largest value, another rounding)
                 assert bool(((v - w).abs() <= 2.0 ** -4 * w.abs() + ref.s[0, 7] * 2.0 ** -9).all())
+
+
+def _rule(v, pow2):
+    """The quantisers' rule on fp32 values [rows, cols], 1x128 groups, rows padded to a
+    multiple of 16; on the CPU, whose divisions are IEEE's. -> codes, scales."""
+    torch = _t()
+    v = torch.nn.functional.pad(v.cpu(), (0, 0, 0, -v.shape[0] % 16))
+    rows, cols = v.shape
+    w = torch.nn.functional.pad(v, (0, -cols % 128)).reshape(rows, -1, 128)
+    amax = w.abs().amax(2)
+    if pow2:
+        m, e = torch.frexp(amax.double() / 448.0)
+        e = torch.where(m > 0.5, e, e - 1).clamp(-127, 120)
+        q, s = torch.ldexp(torch.ones_like(m), -e).float(), torch.ldexp(torch.ones_like(m), e).float()
+        none = amax == 0
+    else:
+        # (a number divided by a tensor is its reciprocal times the number)
+        q, s = torch.full_like(amax, 448.0) / amax, amax / torch.full_like(amax, 448.0)
+        none = (amax == 0) | ~torch.isfinite(q)
+    q, s = (torch.where(none, torch.ones_like(t), t) for t in (q, s))
+    codes = (w * q[:, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return codes.reshape(rows, -1)[:, :cols], s.t()
+
+
+def _same_codes(out, v, pow2):
+    torch = _t()
+    q, s = _rule(v, pow2)
+    assert torch.equal(out.q.cpu(), q) and torch.equal(out.s.cpu(), s)
+    pad = torch.nn.functional.pad(v, (0, 0, 0, -v.shape[0] % 16))
+    q, s = _rule(pad.t().contiguous(), pow2)
+    cols = v.shape[1]
+    assert torch.equal(out.q_t.cpu(), q[:cols]) and torch.equal(out.s_t.cpu(), s[:, :cols])
+
+
+# the forms for few tiles, for ragged widths and for many tiles
+@pytest.mark.parametrize("rows,f", [(33, 144), (777, 1360), (1300, 2000), (2500, 2048), (4100, 640)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_bits_of_the_quantisers_rule(rows, f, pow2):
+    """Gates above 128 have a sigmoid of 1: the products of bf16 values are exact in
+    fp32, and the codes and scales are bit by bit what the quantisers' rule makes of
+    them, whatever their magnitude."""
+    torch, ops = _t(), _ops()
+    g = torch.Generator(device="cuda").manual_seed(70)
+
+    def spread(r, c, low, high):
+        e = torch.randint(low, high, (r, 1), generator=g, device="cuda").float()
+        return torch.ldexp(torch.randn(r, c, generator=g, device="cuda"), e).bfloat16()
+    gate = (128 + 128 * torch.rand(rows, f, generator=g, device="cuda")).bfloat16()
+    up = spread(rows, f, -126, 110)
+    v = gate.float() * up.float()
+    out = ops.swiglu_quantize(torch.cat([gate, up], 1), colwise=True, pow2=pow2)
+    _same_codes(out, v, pow2)
+    row = ops.swiglu_quantize(torch.cat([gate, up], 1), pow2=pow2)
+    assert torch.equal(row.q, out.q) and torch.equal(row.s, out.s)
+    # backward: dgate = da up, dup = da gate (1 - sigmoid is 0)
+    da, up = spread(rows, f, -60, 50), spread(rows, f, -60, 50)
+    d = torch.cat([da.float() * up.float(), da.float() * gate.float()], 1)
+    _same_codes(ops.swiglu_backward_quantize(da, torch.cat([gate, up], 1), pow2=pow2), d, pow2)
