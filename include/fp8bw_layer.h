@@ -46,9 +46,15 @@ extern "C" {
  *   y           : bf16 [rows, cols] (out) or NULL: v rounded to bf16
  *   q, s        : row-wise codes of v (out), both or neither
  *   q_t, s_t    : column-wise codes of v, transposed (out), both or neither
- * cols <= 32768; eps >= 0 (else FP8BW_ERR_SHAPE). The sum of squares is fp32: a
- * row in which it overflows (values around 2^63 and more) has rstd 0; a row of
- * zeros with eps == 0 is not finite, as the formula says. */
+ * cols <= 32768; eps >= 0 (else FP8BW_ERR_SHAPE). The sum of a row's squares is
+ * fp32: rows whose Euclidean norm is in [2^-50, 2^64) are right to a few roundings,
+ * and down to zero rows for eps >= 2^-100. Rows of 2^64 and more (values around
+ * 2^58.5 in all of 2048 columns) have rstd 0; smaller ones than 2^-50 lose bits with
+ * a smaller eps, and are not finite where all squares vanish (as a row of zeros is
+ * with eps == 0, by the formula).
+ * The two products are taken in the order above, or with rstd last where nothing
+ * leaves fp32's range on the way; a factor that a group's or a column's values share
+ * joins their scale's. */
 int fp8bw_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual,
                            const void* gamma, int gamma_is_f32, int64_t rows,
                            int64_t cols, float eps, uint16_t* h, float* rstd,
@@ -69,6 +75,7 @@ int fp8bw_rmsnorm_quantize_pow2(const uint16_t* x, const uint16_t* residual,
  *   dy, h, dres : bf16 [rows, cols];  rstd : fp32 [rows]
  *   dh          : bf16 [rows, cols] (out);  dgamma : fp32 [cols] (out)
  *   workspace   : at least fp8bw_rmsnorm_backward_workspace(rows, cols) bytes
+ * fp32 throughout: rstd^2 has to be a normal number (rstd in 2^-63 .. 2^63).
  * The sum over rows is taken in a fixed order: equal inputs give equal bits.
  * rows == 0 writes dgamma = 0. */
 int64_t fp8bw_rmsnorm_backward_workspace(int64_t rows, int64_t cols);

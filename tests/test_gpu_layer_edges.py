@@ -303,3 +303,34 @@ def test_bits_of_the_quantisers_rule(rows, f, pow2):
     da, up = spread(rows, f, -60, 50), spread(rows, f, -60, 50)
     d = torch.cat([da.float() * up.float(), da.float() * gate.float()], 1)
     _same_codes(ops.swiglu_backward_quantize(da, torch.cat([gate, up], 1), pow2=pow2), d, pow2)
+
+
+@pytest.mark.parametrize("cols", [16, 2048, 8192, 32768])
+@pytest.mark.parametrize("residual", [False, True])
+def test_the_range_of_the_norm(cols, residual):
+    """Rows of a Euclidean norm from 2^-50 to 2^64 without eps, and beyond."""
+    torch, ops = _t(), _ops()
+    x = _normal((48, cols), 80, 1.0, torch.float32)
+    x = x / x.double().norm(dim=1, keepdim=True).float()
+    size = torch.linspace(-49.9, 63.9, 48, device="cuda", dtype=torch.float64).exp2()
+    x = (x * size[:, None]).bfloat16()
+    r = torch.zeros_like(x) if residual else None
+    gamma = 1 + _normal((cols,), 81, 0.2)
+    _, rstd, v, err = R.norm(x, r, gamma, 0.0)
+    out = ops.rmsnorm_quantize(x, gamma, r, 0.0, colwise=True)
+    assert bool(((out.rstd.double() - rstd).abs() <= R.NORM_REL * rstd).all())
+    R.check_codes(out.q, out.s, v, err, 1, False, 48)
+    R.check_codes(out.q_t, out.s_t, v, err, 0, False, 48)
+    # beyond: zeros, and the rows beside them as they were
+    y = x.clone()
+    y[4] = (x[47].double() * 2).bfloat16()        # 2^64.9
+    got = ops.rmsnorm_quantize(y, gamma, r, 0.0)
+    assert float(got.rstd[4]) == 0 and not bool(_values(got.q[4]).ne(0).any())
+    keep = [i for i in range(48) if i != 4]
+    assert torch.equal(got.q[keep], out.q[keep]) and torch.equal(got.rstd[keep], out.rstd[keep])
+    # with an eps that matters, any smaller row
+    y = (x[:16].double() * 2.0 ** -70).bfloat16()
+    h, rstd, v, err = R.norm(y, r[:16] if residual else None, gamma, 1e-6)
+    got = ops.rmsnorm_quantize(y, gamma, r[:16] if residual else None, 1e-6)
+    assert bool(((got.rstd.double() - rstd).abs() <= R.NORM_REL * rstd).all())
+    R.check_codes(got.q, got.s, v, err, 1, False, 16)
