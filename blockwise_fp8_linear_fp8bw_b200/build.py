@@ -8,6 +8,7 @@ cudaGetDriverEntryPoint, so no libcuda link is needed at build time. Besides,
 one CPython extension module (csrc/layer/binding.cpp, host code) that gives the
 layer operators' Python calls a short path.
 """
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -36,14 +37,32 @@ def _sources():
 
 
 # The Python binding of the layer operators: a CPython extension module, host
-# code only, compiled against the installed torch.
+# code only, compiled against the installed torch. It calls the library through the
+# header's types and torch through its C++ interface, so either one's change rebuilds
+# it; the torch version it was compiled for stands in the module.
 BINDING_SRC = os.path.join(CSRC, "layer", "binding.cpp")
 BINDING = os.path.join(HERE, "_layer_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
+def _torch_version():
+    """The installed torch's version (without importing it), or None."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
 def _binding_stale() -> bool:
-    return not os.path.exists(BINDING) or \
-        os.path.getmtime(BINDING_SRC) > os.path.getmtime(BINDING)
+    version = _torch_version()
+    if version is None:          # nothing to bind to: the library is all there is
+        return False
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    if any(os.path.getmtime(s) > t for s in (BINDING_SRC, HEADER, LAYER_HEADER)):
+        return True
+    with open(BINDING, "rb") as fh:
+        return ("fp8bw binding for torch %s\0" % version).encode() not in fh.read()
 
 
 def build_binding(force: bool = False) -> str:
@@ -56,6 +75,7 @@ def build_binding(force: bool = False) -> str:
     tmp = BINDING + ".tmp.%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DFP8BW_TORCH_VERSION="%s"' % _torch_version(),
            "-I" + os.path.join(root, "include"),
            "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
@@ -89,9 +109,14 @@ def _lib_stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force)
-    if not force and not _lib_stale():
-        return LIB
+    if force or _lib_stale():
+        _build_lib(verbose)
+    if _torch_version() is not None:
+        build_binding(force)
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [_nvcc()] + NVCC_FLAGS + ["-o", tmp] + UNITS
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -104,7 +129,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stdout.write(log)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -18,40 +18,37 @@
 #include <cstdint>
 #include <stdexcept>
 #include <string>
+#include <type_traits>
 #include <vector>
+
+#include "../../../include/fp8bw_layer.h"
 
 namespace {
 
-using RmsNorm = int (*)(const void*, const void*, const void*, int, int64_t, int64_t, float, void*,
-                        float*, void*, void*, float*, void*, float*, void*);
-using RmsNormBwdWs = int64_t (*)(int64_t, int64_t);
-using RmsNormBwd = int (*)(const void*, const void*, const float*, const void*, int, const void*,
-                           int64_t, int64_t, void*, float*, void*, int64_t, void*);
-using Swiglu = int (*)(const void*, int64_t, int64_t, void*, float*, void*, float*, void*);
-using SwigluBwd = int (*)(const void*, const void*, int64_t, int64_t, void*, float*, void*, float*,
-                          void*);
-
-struct NsJob {       // fp8bw_ns_job
-  const void* g;
-  int64_t n, k;
-  void* out;
-};
-using NewtonSchulzWs = int64_t (*)(const NsJob*, int);
-using NewtonSchulz = int (*)(const NsJob*, int, int, int, float, float, float, float, void*,
-                             int64_t, void*);
+using NsJob = fp8bw_ns_job;
 
 constexpr int kFunctions = 10;
-constexpr Py_ssize_t kNsJobs = 8;      // matrices per call of the library
+constexpr Py_ssize_t kNsJobs = FP8BW_NS_MAX_JOBS;
 
-struct Library {
-  RmsNorm rmsnorm[2];          // by pow2
-  RmsNormBwdWs rmsnorm_bwd_ws;
-  RmsNormBwd rmsnorm_bwd;
-  Swiglu swiglu[2];
-  SwigluBwd swiglu_bwd[2];
-  NewtonSchulzWs ns_ws;
-  NewtonSchulz ns;
+struct Library {               // the types are the header's
+  decltype(&fp8bw_rmsnorm_quantize) rmsnorm[2];          // by pow2
+  decltype(&fp8bw_rmsnorm_backward_workspace) rmsnorm_bwd_ws;
+  decltype(&fp8bw_rmsnorm_backward) rmsnorm_bwd;
+  decltype(&fp8bw_swiglu_quantize) swiglu[2];
+  decltype(&fp8bw_swiglu_backward_quantize) swiglu_bwd[2];
+  decltype(&fp8bw_newton_schulz_workspace) ns_ws;
+  decltype(&fp8bw_newton_schulz) ns;
 } lib;
+static_assert(std::is_same<decltype(&fp8bw_rmsnorm_quantize),
+                           decltype(&fp8bw_rmsnorm_quantize_pow2)>::value &&
+              std::is_same<decltype(&fp8bw_swiglu_quantize),
+                           decltype(&fp8bw_swiglu_quantize_pow2)>::value &&
+              std::is_same<decltype(&fp8bw_swiglu_backward_quantize),
+                           decltype(&fp8bw_swiglu_backward_quantize_pow2)>::value,
+              "the two scale rules' functions are called through one type");
+
+// What the module was compiled against, for the build to find in the file.
+__attribute__((used)) const char kBuiltFor[] = "fp8bw binding for torch " FP8BW_TORCH_VERSION;
 
 // A refused argument (ValueError in Python).
 struct Refused : std::runtime_error {
@@ -86,6 +83,11 @@ void* input(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, con
   return t.data_ptr();
 }
 
+const uint16_t* bf16_input(const at::Tensor& t, at::IntArrayRef shape, const char* name,
+                           const at::Device& dev) {
+  return static_cast<const uint16_t*>(input(t, at::kBFloat16, shape, name, dev));
+}
+
 // rows, cols of a 2-D bf16 tensor.
 at::IntArrayRef matrix(const at::Tensor& t, const char* name) {
   if (t.scalar_type() != at::kBFloat16 || t.dim() != 2)
@@ -107,6 +109,8 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& d
 
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 float* fptr(const at::Tensor& t) { return static_cast<float*>(ptr(t)); }
+uint16_t* hptr(const at::Tensor& t) { return static_cast<uint16_t*>(ptr(t)); }   // bf16
+uint8_t* bptr(const at::Tensor& t) { return static_cast<uint8_t*>(ptr(t)); }
 
 void* stream_of(const at::Device& dev) {
   return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
@@ -150,7 +154,8 @@ struct NormInputs {
   at::Device dev;
   int64_t rows, cols;
   int gamma_f32;
-  const void *x, *gamma, *residual = nullptr;
+  const uint16_t *x, *residual = nullptr;
+  const void* gamma;
   NormInputs(PyObject* ox, PyObject* og, PyObject* orr, const char* nx, const char* nr)
       : dev(at::kCPU) {
     const at::Tensor& tx = tensor(ox, nx);
@@ -164,9 +169,9 @@ struct NormInputs {
       throw Refused("gamma: expected bf16 or fp32 (" + std::to_string(cols) + ",), got " +
                     at::toString(gt) + " " + shape_text(tg.sizes()));
     gamma_f32 = gt == at::kFloat;
-    x = input(tx, at::kBFloat16, shape, nx, dev);
+    x = bf16_input(tx, shape, nx, dev);
     gamma = input(tg, gt, tg.sizes(), "gamma", dev);
-    if (orr != Py_None) residual = input(tensor(orr, nr), at::kBFloat16, shape, nr, dev);
+    if (orr != Py_None) residual = bf16_input(tensor(orr, nr), shape, nr, dev);
   }
 };
 
@@ -214,18 +219,18 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor h = in.residual == nullptr ? tensor(a[0], "x")
                                           : empty({in.rows, in.cols}, at::kBFloat16, in.dev);
     at::Tensor rstd = empty({in.rows}, at::kFloat, in.dev), y;
-    void* ph = in.residual == nullptr ? nullptr : h.data_ptr();
+    uint16_t* ph = in.residual == nullptr ? nullptr : hptr(h);
     if (!truth(a[4])) {
       y = empty({in.rows, in.cols}, at::kBFloat16, in.dev);
       const int st = lib.rmsnorm[0](in.x, in.residual, in.gamma, in.gamma_f32, in.rows, in.cols,
-                                    static_cast<float>(eps), ph, fptr(rstd), ptr(y), nullptr,
+                                    static_cast<float>(eps), ph, fptr(rstd), hptr(y), nullptr,
                                     nullptr, nullptr, nullptr, stream_of(in.dev));
       return result(st, {y, h, rstd});
     }
     const Codes c(in.rows, in.cols, in.dev, truth(a[5]));
     const int st = lib.rmsnorm[truth(a[6])](
         in.x, in.residual, in.gamma, in.gamma_f32, in.rows, in.cols, static_cast<float>(eps), ph,
-        fptr(rstd), nullptr, ptr(c.q), fptr(c.s), ptr(c.q_t), fptr(c.s_t), stream_of(in.dev));
+        fptr(rstd), nullptr, bptr(c.q), fptr(c.s), bptr(c.q_t), fptr(c.s_t), stream_of(in.dev));
     return result(st, {c.q, c.s, c.q_t, c.s_t, h, rstd});
   });
 }
@@ -236,7 +241,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const NormInputs in(a[1], a[3], a[4], "h", "dres");
     const int64_t shape[2] = {in.rows, in.cols};
-    const void* dy = input(tensor(a[0], "dy"), at::kBFloat16, shape, "dy", in.dev);
+    const uint16_t* dy = bf16_input(tensor(a[0], "dy"), shape, "dy", in.dev);
     const void* rstd = input(tensor(a[2], "rstd"), at::kFloat, {in.rows}, "rstd", in.dev);
     need_cuda(in.dev);
     const int64_t size = lib.rmsnorm_bwd_ws(in.rows, in.cols);
@@ -246,7 +251,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor dgamma = empty({in.cols}, at::kFloat, in.dev);
     const at::Tensor ws = empty({size}, at::kByte, in.dev);
     const int st = lib.rmsnorm_bwd(dy, in.x, static_cast<const float*>(rstd), in.gamma,
-                                   in.gamma_f32, in.residual, in.rows, in.cols, ptr(dh),
+                                   in.gamma_f32, in.residual, in.rows, in.cols, hptr(dh),
                                    fptr(dgamma), ptr(ws), size, stream_of(in.dev));
     return result(st, {dh, dgamma});
   });
@@ -266,11 +271,11 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef shape = matrix(gu, "gu");
     const int64_t f = half_of(shape);
     const at::Device dev = gu.device();
-    const void* p = input(gu, at::kBFloat16, shape, "gu", dev);
+    const uint16_t* p = bf16_input(gu, shape, "gu", dev);
     need_cuda(dev);
     const c10::cuda::CUDAGuard guard(dev);
     const Codes c(shape[0], f, dev, truth(a[1]));
-    const int st = lib.swiglu[truth(a[2])](p, shape[0], f, ptr(c.q), fptr(c.s), ptr(c.q_t),
+    const int st = lib.swiglu[truth(a[2])](p, shape[0], f, bptr(c.q), fptr(c.s), bptr(c.q_t),
                                            fptr(c.s_t), stream_of(dev));
     return result(st, {c.q, c.s, c.q_t, c.s_t});
   });
@@ -284,13 +289,13 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef shape = matrix(gu, "gu");
     const int64_t f = half_of(shape);
     const at::Device dev = gu.device();
-    const void* pg = input(gu, at::kBFloat16, shape, "gu", dev);
-    const void* pd = input(tensor(a[0], "da"), at::kBFloat16, {shape[0], f}, "da", dev);
+    const uint16_t* pg = bf16_input(gu, shape, "gu", dev);
+    const uint16_t* pd = bf16_input(tensor(a[0], "da"), {shape[0], f}, "da", dev);
     need_cuda(dev);
     const c10::cuda::CUDAGuard guard(dev);
     const Codes c(shape[0], 2 * f, dev, true);
-    const int st = lib.swiglu_bwd[truth(a[2])](pd, pg, shape[0], f, ptr(c.q), fptr(c.s),
-                                               ptr(c.q_t), fptr(c.s_t), stream_of(dev));
+    const int st = lib.swiglu_bwd[truth(a[2])](pd, pg, shape[0], f, bptr(c.q), fptr(c.s),
+                                               bptr(c.q_t), fptr(c.s_t), stream_of(dev));
     return result(st, {c.q, c.s, c.q_t, c.s_t});
   });
 }
@@ -337,7 +342,7 @@ PyObject* newton_schulz(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(dev);
     for (Py_ssize_t i = 0; i < count; ++i) {
       outs[i] = empty({jobs[i].n, jobs[i].k}, at::kBFloat16, dev);
-      jobs[i].out = outs[i].data_ptr();
+      jobs[i].out = hptr(outs[i]);
     }
     const at::Tensor ws = empty({size}, at::kByte, dev);
     int st = 0;
@@ -365,16 +370,17 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return nullptr;
     }
   }
-  lib.rmsnorm[0] = reinterpret_cast<RmsNorm>(p[0]);
-  lib.rmsnorm[1] = reinterpret_cast<RmsNorm>(p[1]);
-  lib.rmsnorm_bwd_ws = reinterpret_cast<RmsNormBwdWs>(p[2]);
-  lib.rmsnorm_bwd = reinterpret_cast<RmsNormBwd>(p[3]);
-  lib.swiglu[0] = reinterpret_cast<Swiglu>(p[4]);
-  lib.swiglu[1] = reinterpret_cast<Swiglu>(p[5]);
-  lib.swiglu_bwd[0] = reinterpret_cast<SwigluBwd>(p[6]);
-  lib.swiglu_bwd[1] = reinterpret_cast<SwigluBwd>(p[7]);
-  lib.ns_ws = reinterpret_cast<NewtonSchulzWs>(p[8]);
-  lib.ns = reinterpret_cast<NewtonSchulz>(p[9]);
+  auto set = [](auto& fn, void* at) { fn = reinterpret_cast<std::decay_t<decltype(fn)>>(at); };
+  set(lib.rmsnorm[0], p[0]);
+  set(lib.rmsnorm[1], p[1]);
+  set(lib.rmsnorm_bwd_ws, p[2]);
+  set(lib.rmsnorm_bwd, p[3]);
+  set(lib.swiglu[0], p[4]);
+  set(lib.swiglu[1], p[5]);
+  set(lib.swiglu_bwd[0], p[6]);
+  set(lib.swiglu_bwd[1], p[7]);
+  set(lib.ns_ws, p[8]);
+  set(lib.ns, p[9]);
   Py_RETURN_NONE;
 }
 

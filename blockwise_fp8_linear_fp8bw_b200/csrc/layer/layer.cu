@@ -458,6 +458,7 @@ int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t row
 
 // ---------------------------------------------------------------- Newton-Schulz
 constexpr int kMaxSteps = 64;
+static_assert(ns::kMaxJobs == FP8BW_NS_MAX_JOBS, "the header's limit");
 constexpr int64_t kMaxNsDim = int64_t(1) << 17;
 
 struct NsBuffers {

@@ -113,7 +113,8 @@ int fp8bw_swiglu_backward_quantize_pow2(const uint16_t* da, const uint16_t* gu,
                                         void* stream);
 
 /* Orthogonalisation of weight updates by Newton-Schulz products (the update
- * rule of the Muon optimiser), for up to 8 matrices of any shapes at once:
+ * rule of the Muon optimiser), for up to FP8BW_NS_MAX_JOBS matrices of any shapes at
+ * once:
  *   X = G / (||G||_F + eps), then `steps` times
  *   X <- a X + b (X X^T) X + c (X X^T)^2 X
  * (grouped on the shorter side; two consecutive steps may be taken as one there).
@@ -122,12 +123,14 @@ int fp8bw_swiglu_backward_quantize_pow2(const uint16_t* da, const uint16_t* gu,
  * singular values of X below 4 and those of b A + c A^2 (A = X X^T) below 15,
  * as the usual coefficients (3.4445, -4.7750, 2.0315) do: beyond, fp16
  * overflows and the result is not finite.
- *   jobs      : HOST array of `count` (0..8) descriptions
+ *   jobs      : HOST array of `count` (0..FP8BW_NS_MAX_JOBS) descriptions
  *   g_is_f32  : every g is fp32 (!= 0) or bf16 (0)
  *   steps     : 1..64
  *   workspace : at least fp8bw_newton_schulz_workspace(jobs, count) bytes,
  *               128-byte aligned
  * n and k are multiples of 16, at most 2^17; an empty matrix is a no-op. */
+#define FP8BW_NS_MAX_JOBS 8
+
 typedef struct fp8bw_ns_job {
     const void* g;       /* [n, k], fp32 or bf16                             */
     int64_t n, k;
