@@ -31,11 +31,19 @@ def _pad_tokens(t):
     return torch.nn.functional.pad(t, (0, 0, 0, extra)) if extra else t
 
 
+def _first_rows(t, n):
+    """The first n rows of `t`, just made here, as a tensor of their own and not a view
+    of it: what a Function returns may be changed in place, a view would not."""
+    if t.shape[0] == n:
+        return t
+    return t.new_empty(0).set_(t.untyped_storage(), 0, (n, t.shape[1]), t.stride())
+
+
 def _bf16_rows(t, k, name):
     if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape[-1] != k:
         raise ValueError("%s: expected a bf16 CUDA tensor with %d features, got %s %s on %s"
                          % (name, k, t.dtype, tuple(t.shape), t.device))
-    return t.reshape(-1, k).contiguous()
+    return (t if t.dim() == 2 else t.reshape(-1, k)).contiguous()
 
 
 class BlockwiseFp8MLPFunction(torch.autograd.Function):
@@ -49,7 +57,7 @@ class BlockwiseFp8MLPFunction(torch.autograd.Function):
             [w_gate_up.contiguous(), w_down.contiguous()], pow2=pow2)
         gu = ops.gemm_fprop(n.q, n.s, qw1, sw1, pow2=pow2)
         a = ops.swiglu_quantize(gu, colwise=True, pow2=pow2)
-        y = ops.gemm_fprop(a.q, a.s, qw2, sw2, pow2=pow2)[:x.shape[0]]
+        y = _first_rows(ops.gemm_fprop(a.q, a.s, qw2, sw2, pow2=pow2), x.shape[0])
         ctx.save_for_backward(n.h, n.rstd, gamma, n.q_t, n.s_t, gu, a.q_t, a.s_t,
                               qw1_t, sw1, qw2_t, sw2)
         ctx.weights = (w_gate_up, w_down)
@@ -151,7 +159,7 @@ class BlockwiseFp8MLP(torch.nn.Module):
         gu = ops.gemm_fprop(n.q, n.s, qw1, sw1, pow2=self.pow2)
         a = ops.swiglu_quantize(gu, pow2=self.pow2)
         y = ops.gemm_fprop(a.q, a.s, qw2, sw2, pow2=self.pow2)
-        return y[:x.shape[0]], n.h
+        return _first_rows(y, x.shape[0]), n.h
 
     def forward(self, x, residual=None):
         shape = x.shape
@@ -172,7 +180,7 @@ class BlockwiseFp8MLP(torch.nn.Module):
         else:
             y, h = BlockwiseFp8MLPFunction.apply(x2, r2, self.gamma, self.w_gate_up,
                                                  self.w_down, self.eps, self.pow2)
-        return y.reshape(shape), h.reshape(shape)
+        return (y, h) if len(shape) == 2 else (y.reshape(shape), h.reshape(shape))
 
     def extra_repr(self):
         return "hidden=%d, ffn=%d, eps=%g, pow2=%s" % (self.hidden, self.ffn, self.eps, self.pow2)
