@@ -11,7 +11,9 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include <algorithm>
 #include <climits>
@@ -359,6 +361,21 @@ PyObject* newton_schulz(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (leaf) -> whether its gradient accumulator is alive, held by an earlier graph, and
+// belongs to the device's default stream.
+PyObject* accumulates_on_default_stream(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 1)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& t = tensor(a[0], "leaf");
+    need_cuda(t.device());
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+    const auto stream = node == nullptr ? std::nullopt : node->stream();
+    return PyBool_FromLong(stream.has_value() && stream->device_type() == at::kCUDA &&
+                           c10::cuda::CUDAStream(*stream) ==
+                               c10::cuda::getDefaultCUDAStream(t.device().index()));
+  });
+}
+
 // Addresses of the library's functions, in the order of Library.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, kFunctions)) return nullptr;
@@ -392,6 +409,7 @@ PyMethodDef methods[] = {
     {"swiglu", FAST(swiglu), METH_FASTCALL, nullptr},
     {"swiglu_backward", FAST(swiglu_backward), METH_FASTCALL, nullptr},
     {"newton_schulz", FAST(newton_schulz), METH_FASTCALL, nullptr},
+    {"accumulates_on_default_stream", FAST(accumulates_on_default_stream), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

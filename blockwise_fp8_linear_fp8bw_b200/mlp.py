@@ -46,6 +46,22 @@ def _bf16_rows(t, k, name):
     return (t if t.dim() == 2 else t.reshape(-1, k)).contiguous()
 
 
+def _refuse_mixed_capture(ctx):
+    """Under capture: raise if the gradient of one of the block's leaves is accumulated
+    on the default stream, by a node that a graph made there still holds. Autograd would
+    have the two streams wait for one another, which ends the capture and, from its
+    worker thread, the process."""
+    if not torch.cuda.is_current_stream_capturing():
+        return
+    for node, _ in ctx.next_functions:
+        leaf = getattr(node, "variable", None)
+        if leaf is not None and ops.accumulates_on_default_stream(leaf):
+            raise RuntimeError(
+                "BlockwiseFp8MLP: a graph made on the default stream still holds a %s leaf "
+                "of this backward pass; let go of it, or warm up on the stream that captures"
+                % (tuple(leaf.shape),))
+
+
 class BlockwiseFp8MLPFunction(torch.autograd.Function):
     """(x, residual, gamma, w_gate_up, w_down) -> (y, h), or y alone without a
     residual (h is x then); see the module docstring. 2-D x and residual."""
@@ -69,6 +85,7 @@ class BlockwiseFp8MLPFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh=None):
+        _refuse_mixed_capture(ctx)
         (h, rstd, gamma, qx_t, sx_t, gu, qa_t, sa_t, qw1_t, sw1, qw2_t,
          sw2) = ctx.saved_tensors
         pow2, weights = ctx.pow2, ctx.weights
@@ -122,9 +139,9 @@ class BlockwiseFp8MLP(torch.nn.Module):
     the weights' codes for the calls that follow (until `unfreeze()`).
 
     A training step can be captured into a CUDA graph. Warm up on the stream that
-    will capture, and let go of what eager steps returned before capturing: an
-    eager graph that still holds the leaves has autograd synchronise with its
-    stream, which a capture does not allow."""
+    will capture, or let go of what eager steps returned before capturing: while a
+    graph made on the default stream holds the leaves, autograd would synchronise with
+    that stream, and the captured backward pass raises instead."""
 
     def __init__(self, hidden, ffn, eps=1e-6, device=None, pow2=False):
         super().__init__()

@@ -488,6 +488,12 @@ def fp8bw_swiglu_backward_quantize(da, gu, q, s, q_t, s_t, stream=None,
           _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t))
 
 
+def accumulates_on_default_stream(leaf):
+    """Whether a graph that is still alive has the gradient of `leaf` (a CUDA tensor)
+    accumulated on its device's default stream."""
+    return _fast.accumulates_on_default_stream(leaf)
+
+
 def _workspace_size(name, *args):
     size = getattr(_lib, name)(*args)
     if size < 0:

@@ -51,3 +51,41 @@ def test_the_output_may_be_changed_in_place(shape, residual):
         y = y if len(shape) == 2 else y.clone()
     y += add
     assert torch.equal(y.detach(), ys[0])
+
+
+def test_a_captured_backward_pass_beside_an_eager_graph():
+    """It is refused while a graph of the default stream holds the leaves, with the
+    process and the device as they were, and works once that graph is gone."""
+    torch, mlp = _mods()
+    m = _block(torch, mlp)
+    x, r, dy = _inputs(torch, (32, 272), 2)
+    x.requires_grad_()
+    for w in (m.w_gate_up, m.w_down):
+        w.main_grad = torch.zeros(w.shape, device="cuda")
+
+    def step():
+        y, h = m(x, r)
+        return torch.autograd.grad([y, h], [x, m.gamma], [dy, dy])
+
+    s = torch.cuda.Stream()
+    held = m(x, r)                                # on the default stream, kept
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = step()                             # eager, on another stream: fine
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="default stream still holds"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, step()))
+    del held
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = step()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    del g
