@@ -56,8 +56,9 @@ class MuonH(torch.optim.Optimizer):
             w = p.detach().float()
             state["momentum"] = torch.zeros_like(w)
             state["radius"] = torch.linalg.vector_norm(w)
-            if p.dtype != torch.float32:
-                state["master"] = w.clone()
+        if p.dtype != torch.float32 and "master" not in state:
+            # (nor has the state of a run whose weights were fp32)
+            state["master"] = p.detach().float().clone()
         return state
 
     @torch.no_grad()
