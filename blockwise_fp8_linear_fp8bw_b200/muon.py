@@ -18,7 +18,7 @@ from . import ops
 
 
 class MuonH(torch.optim.Optimizer):
-    """Optimiser of 2-D weights [n, k] with sides that are multiples of 16.
+    """Optimiser of 2-D weights [n, k] with sides that are multiples of 16, up to 2^17.
 
     `project=False` leaves the projection out (plain Muon)."""
 
@@ -32,10 +32,10 @@ class MuonH(torch.optim.Optimizer):
     def add_param_group(self, group):
         super().add_param_group(group)
         for p in self.param_groups[-1]["params"]:
-            if p.dim() != 2 or p.shape[0] % 16 or p.shape[1] % 16:
+            if p.dim() != 2 or p.shape[0] % 16 or p.shape[1] % 16 or max(p.shape) > 1 << 17:
                 del self.param_groups[-1]
                 raise ValueError("MuonH takes 2-D weights with sides that are multiples of "
-                                 "16, got %s" % (tuple(p.shape),))
+                                 "16 and at most 2^17, got %s" % (tuple(p.shape),))
 
     def load_state_dict(self, state_dict):
         super().load_state_dict(state_dict)
@@ -49,15 +49,16 @@ class MuonH(torch.optim.Optimizer):
 
     def _state_of(self, p, group):
         state = self.state[p]
+        # (the state of a run whose weights were fp32 has no master)
+        master = p.dtype != torch.float32 and "master" not in state
+        if (not state or master) and torch.cuda.is_current_stream_capturing():
+            # a replay would start from the captured state every time
+            raise RuntimeError("MuonH: take one step before capturing one in a graph")
         if not state:
-            if torch.cuda.is_current_stream_capturing():
-                # a replay would start from the captured state every time
-                raise RuntimeError("MuonH: take one step before capturing one in a graph")
             w = p.detach().float()
             state["momentum"] = torch.zeros_like(w)
             state["radius"] = torch.linalg.vector_norm(w)
-        if p.dtype != torch.float32 and "master" not in state:
-            # (nor has the state of a run whose weights were fp32)
+        if master:
             state["master"] = p.detach().float().clone()
         return state
 
@@ -67,15 +68,24 @@ class MuonH(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        work = []              # (group, [(weight, gradient)]) of one device
         for group in self.param_groups:
-            todo = {}          # device -> [(weight, gradient)]
+            todo = {}
             for p in group["params"]:
                 g = getattr(p, "main_grad", None)
                 g = p.grad if g is None else g
-                if g is not None:
-                    todo.setdefault(p.device, []).append((p, g))
-            for pairs in todo.values():
-                self._step_device(group, pairs)
+                if g is None:
+                    continue
+                # (before any state changes)
+                if not p.is_cuda or g.device != p.device or g.shape != p.shape or g.is_sparse:
+                    raise ValueError(
+                        "MuonH steps CUDA weights with dense gradients of their shape and "
+                        "device, got a weight %s on %s and a gradient %s on %s"
+                        % (tuple(p.shape), p.device, tuple(g.shape), g.device))
+                todo.setdefault(p.device, []).append((p, g))
+            work += [(group, pairs) for pairs in todo.values()]
+        for group, pairs in work:
+            self._step_device(group, pairs)
         return loss
 
     def _step_device(self, group, pairs):
