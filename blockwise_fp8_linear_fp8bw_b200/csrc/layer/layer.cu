@@ -284,7 +284,8 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
     p.v = v;
     p.r = v == 1 ? 2 : 1;
     p.tpr = threads_per_row(chunks, v);
-    p.groups = std::max(1, 128 / std::max(p.tpr, 1));
+    // (the kernel adds the groups' partial sums up with one chunk per thread only)
+    p.groups = v == 1 ? std::max(1, 128 / std::max(p.tpr, 1)) : 1;
     p.per_sm = std::max(1, kBwdSmThreads / std::max(p.groups * p.tpr, 1));
     return p;
   };
@@ -435,7 +436,7 @@ int swiglu_backward_quantize(const uint16_t* da, const uint16_t* gu, int64_t row
     const GluRaggedArgs r{gu, da, rows, f,
                           GluTileArgs{tiles_r, static_cast<int>(cdiv(2 * f, 128)), out}};
     return launched(launch_kernel(swiglu_bwd_ragged_kernel<POW2>, dim3(glu_tiles(out)), block,
-                                  TileEmit<1, true, false>::kBytes + 128, cs, r));
+                                  TileEmit<1, false>::kBytes + 128, cs, r));
   }
   CUtensorMap mg, mu, md;
   st = encode_tiles(&mg, gu, rows, f, 4 * f);

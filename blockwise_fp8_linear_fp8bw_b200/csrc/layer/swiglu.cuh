@@ -198,7 +198,7 @@ constexpr int kGluFwdSlots = 6;
 using GluFwdRing = TileRing<4, kGluFwdSlots>;      // gate, up, twice
 struct GluFwdSmem {
   static constexpr int kEmit = (GluFwdRing::kBytes + 127) / 128 * 128;
-  static constexpr int kAlloc = kEmit + TileEmit<2, true, false>::kBytes + 128;
+  static constexpr int kAlloc = kEmit + TileEmit<2, false>::kBytes + 128;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
 
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tmap(&map_g);
     prefetch_tmap(&map_u);
   }
-  TileEmit<2, true, POW2>::init(smem + GluFwdSmem::kEmit);
+  TileEmit<2, POW2>::init(smem + GluFwdSmem::kEmit);
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tma_load_2d(dst, n % 2 == 0 ? &map_g : &map_u, bar, tc * kTile, (tile / half) * kTile);
   };
   if (threadIdx.x == 0) ring.fill(kGluFwdSlots, load);
-  TileEmit<2, true, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
+  TileEmit<2, POW2> emit(smem + GluFwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
     float y[2][8][4];
@@ -259,7 +259,7 @@ constexpr int kGluBwdSlots = 6;
 using GluBwdRing = TileRing<3, kGluBwdSlots>;
 struct GluBwdSmem {
   static constexpr int kEmit = (GluBwdRing::kBytes + 127) / 128 * 128;
-  static constexpr int kAlloc = kEmit + TileEmit<2, true, false>::kBytes + 128;
+  static constexpr int kAlloc = kEmit + TileEmit<2, false>::kBytes + 128;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
 
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tmap(&map_u);
     prefetch_tmap(&map_da);
   }
-  TileEmit<2, true, POW2>::init(smem + GluBwdSmem::kEmit);
+  TileEmit<2, POW2>::init(smem + GluBwdSmem::kEmit);
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 (tile / a.tiles_c) * kTile);
   };
   if (threadIdx.x == 0) ring.fill(kGluBwdSlots, load);
-  TileEmit<2, true, POW2> emit(smem + GluBwdSmem::kEmit, a.out);
+  TileEmit<2, POW2> emit(smem + GluBwdSmem::kEmit, a.out);
   for (int i = 0; i < count; ++i) {
     const int tile = static_cast<int>(blockIdx.x + i * gridDim.x);
     const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
@@ -333,7 +333,7 @@ constexpr int kGluRun = 16;
 using GluShiftRing = TileRing<3, kGluShiftSlots>;
 struct GluShiftSmem {
   static constexpr int kEmit = (GluShiftRing::kBytes + 127) / 128 * 128;
-  static constexpr int kKept = kEmit + TileEmit<2, true, false>::kBytes;   // half a tile
+  static constexpr int kKept = kEmit + TileEmit<2, false>::kBytes;   // half a tile
   static constexpr int kAlloc = kKept + kTile * kTile * 2 + 128;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tmap(&map_u);
     prefetch_tmap(&map_da);
   }
-  TileEmit<2, true, POW2>::init(smem + GluShiftSmem::kEmit);
+  TileEmit<2, POW2>::init(smem + GluShiftSmem::kEmit);
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 t / per_row * kTile);
   };
   if (threadIdx.x == 0) ring.fill(kGluShiftSlots, load);
-  TileEmit<2, true, POW2, true> emit(smem + GluShiftSmem::kEmit, a.out);
+  TileEmit<2, POW2, true> emit(smem + GluShiftSmem::kEmit, a.out);
 
   const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31, rot = r / 4;
   emit.turn = rot;
@@ -475,42 +475,40 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   uint8_t* smem = align128(smem_raw);
   const GluTileArgs& a = r.t;
   const int rb = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int num_tiles = a.tiles_r * a.tiles_c;
-  TileEmit<1, true, POW2>::init(smem);
+  TileEmit<1, POW2>::init(smem);
   __syncthreads();
   launch_dependents();
   grid_dependency_wait();
-  TileEmit<1, true, POW2> emit(smem, a.out);
-  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
-    const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
-    const int64_t c0 = static_cast<int64_t>(tc) * kTile + lane * 4;
-    const bool is_up = c0 >= r.f;
-    const int64_t src = is_up ? c0 - r.f : c0;
-    float y[1][8][4];
+  TileEmit<1, POW2> emit(smem, a.out);
+  const int tile = static_cast<int>(blockIdx.x);
+  const int tr = tile / a.tiles_c, tc = tile % a.tiles_c;
+  const int64_t c0 = static_cast<int64_t>(tc) * kTile + lane * 4;
+  const bool is_up = c0 >= r.f;
+  const int64_t src = is_up ? c0 - r.f : c0;
+  float y[1][8][4];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int64_t row = static_cast<int64_t>(tr) * kTile + rb * 8 + p;
+  for (int p = 0; p < 8; ++p) {
+    const int64_t row = static_cast<int64_t>(tr) * kTile + rb * 8 + p;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[0][p][j] = 0.0f;
-      if (row < r.rows && c0 < 2 * r.f) {
-        const uint16_t* gp = r.gu + row * 2 * r.f + src;
-        const uint2 wg = *reinterpret_cast<const uint2*>(gp);
-        const uint2 wu = *reinterpret_cast<const uint2*>(gp + r.f);
-        const uint2 wd = *reinterpret_cast<const uint2*>(r.da + row * r.f + src);
-        const float g[4] = {bf16_lo(wg.x), bf16_hi(wg.x), bf16_lo(wg.y), bf16_hi(wg.y)};
-        const float u[4] = {bf16_lo(wu.x), bf16_hi(wu.x), bf16_lo(wu.y), bf16_hi(wu.y)};
-        const float d[4] = {bf16_lo(wd.x), bf16_hi(wd.x), bf16_lo(wd.y), bf16_hi(wd.y)};
+    for (int j = 0; j < 4; ++j) y[0][p][j] = 0.0f;
+    if (row < r.rows && c0 < 2 * r.f) {
+      const uint16_t* gp = r.gu + row * 2 * r.f + src;
+      const uint2 wg = *reinterpret_cast<const uint2*>(gp);
+      const uint2 wu = *reinterpret_cast<const uint2*>(gp + r.f);
+      const uint2 wd = *reinterpret_cast<const uint2*>(r.da + row * r.f + src);
+      const float g[4] = {bf16_lo(wg.x), bf16_hi(wg.x), bf16_lo(wg.y), bf16_hi(wg.y)};
+      const float u[4] = {bf16_lo(wu.x), bf16_hi(wu.x), bf16_lo(wu.y), bf16_hi(wu.y)};
+      const float d[4] = {bf16_lo(wd.x), bf16_hi(wd.x), bf16_lo(wd.y), bf16_hi(wd.y)};
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          float dgate[2], dup[2];
-          glu_grad2(g + j, u + j, d + j, dgate, dup);
-          y[0][p][j] = is_up ? dup[0] : dgate[0];
-          y[0][p][j + 1] = is_up ? dup[1] : dgate[1];
-        }
+      for (int j = 0; j < 4; j += 2) {
+        float dgate[2], dup[2];
+        glu_grad2(g + j, u + j, d + j, dgate, dup);
+        y[0][p][j] = is_up ? dup[0] : dgate[0];
+        y[0][p][j + 1] = is_up ? dup[1] : dgate[1];
       }
     }
-    emit.step(y, tr, {tc}, [] {});
   }
+  emit.step(y, tr, {tc}, [] {});
   emit.finish();
 }
 

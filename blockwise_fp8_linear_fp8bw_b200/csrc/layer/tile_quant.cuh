@@ -1,5 +1,5 @@
 // tile_quant.cuh -- E4M3 quantisation of 128x128 tiles of fp32 values that a
-// kernel holds in registers: row-wise codes with 1x128 scales and/or
+// kernel holds in registers: row-wise codes with 1x128 scales and
 // column-wise codes (transposed) with 128x1 scales, with the arithmetic and
 // layouts of the quantisers.
 //
@@ -114,7 +114,7 @@ __device__ __forceinline__ void fadd2(float& p0, float& p1, float x0, float x1, 
       : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
 }
 
-// Where codes and scales go (row-wise ones may be unused).
+// Where codes and scales go (the column-wise ones may be unused).
 struct CodesOut {
   uint8_t* q;          // [rows][cols]
   float* s;            // [ceil(cols/128)][rows]
@@ -139,7 +139,7 @@ __device__ __forceinline__ int emit_t_offset(int k, int u) {
 // between the barriers lie this step's row codes, the last step's transposed
 // codes and (in a few warps) the column scales.
 // With TURN, lane l holds columns 4 l' .. of the second tile, l' = (l + turn) % 32.
-template <int NOUT, bool ROW, bool POW2, bool TURN = false>
+template <int NOUT, bool POW2, bool TURN = false>
 struct TileEmit {
   static constexpr int kT = 0;                                   // NOUT x 16 KB
   // Column maxima, combined by shared-memory atomics on the bits (they are not
@@ -216,10 +216,8 @@ struct TileEmit {
         out.s_t[static_cast<int64_t>(tr) * out.cols + static_cast<int64_t>(c) * kTile + k] = s;
     }
     if (last_tr >= 0) write_transposed();
-    if constexpr (ROW) {
 #pragma unroll
-      for (int n = 0; n < NOUT; ++n) write_rows(y[n], tr, tc[n], lane_of(n));
-    }
+    for (int n = 0; n < NOUT; ++n) write_rows(y[n], tr, tc[n], lane_of(n));
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NOUT; ++n) {
