@@ -19,27 +19,26 @@ namespace layer {
 // 1 / (1 + exp(-x)) of two bf16 values by the approximate exponential and reciprocal
 // (packed arithmetic where the instruction exists). log2(e) is taken as H + L with H of
 // 16 bits: x H is exact, and what x L leaves out, at most 4.4e-4 of exp(-x), is added
-// to first order. Relative error in units of 2^-24, rms and largest, for x in [-4, 4]:
-// 0.8 and 2.7; in [-20, 0] 0.9 and 3 (by the rounded x log2(e): 5.2 and 14; a correctly
-// rounded quotient and CUDA's expf: 0.8 and 2.2). Results that would be subnormal are 0,
-// so below -87 the quotient is 0 (its value there is under 2^-125); at -inf it is 0, so
-// that x * sigmoid(x) is NaN as the formula says. (Of NaN it is 1; what it multiplies
-// is NaN.)
+// to first order. Relative error in units of 2^-24, rms and largest, over the bf16 x in
+// [-4, 4]: 0.9 and 3.0; in [-80, 0] 1.1 and 3.4 (by the rounded product x log2(e) 5 and
+// 14 down to -20, 28 and 55 down to -80; by expf and an IEEE quotient 0.8 and 2.3).
+// Results that would be subnormal are 0, so below -87 the quotient is 0 (its value there
+// is under 2^-125); at -inf it is 0, so that x * sigmoid(x) is NaN as the formula says.
+// (Of NaN it is 1; what it multiplies is NaN.)
 __device__ __forceinline__ void sigmoid2(float x0, float x1, float& s0, float& s1) {
   constexpr double kLog2e = 1.4426950408889634, kH = 47274.0 / 32768.0;
   constexpr float h = static_cast<float>(kH);
   constexpr float k = static_cast<float>(-(kLog2e - kH) * 0.6931471805599453 / kH);
-  float p0, p1, e0, e1, t0, t1;
+  float p0, p1, e0, e1, t0 = 1.0f, t1 = 1.0f, d0 = 1.0f, d1 = 1.0f;
   fmul2(p0, p1, x0, x1, h, h);
   p0 = fminf(p0, 150.0f);                     // (infinity times 0 is NaN below)
   p1 = fminf(p1, 150.0f);
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(-p0));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-p1));
-  fmul2(t0, t1, p0, p1, k, k);
-  ffma2(e0, e1, e0, e1, t0, t1);
-  fadd2(e0, e1, e0, e1, 1.0f, 1.0f);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(e0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(e1));
+  ffma2(t0, t1, p0, p1, k, k);
+  ffma2(d0, d1, e0, e1, t0, t1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(d1));
 }
 
 // y = gate * sigmoid(gate) * up, two elements (in this order nothing overflows

@@ -103,17 +103,6 @@ __device__ __forceinline__ float warp_max_abs(float v) {
   return r;
 }
 
-__device__ __forceinline__ void fadd2(float& p0, float& p1, float x0, float x1, float y0,
-                                      float y1) {
-  asm("{\n\t.reg .b64 p, x, y;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 p, x, y;\n\t"
-      "mov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(p0), "=f"(p1)
-      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
-}
-
 // Where codes and scales go (the column-wise ones may be unused).
 struct CodesOut {
   uint8_t* q;          // [rows][cols]
