@@ -524,10 +524,12 @@ int64_t ns_tiles(const NsGemm& g, int bn) {
 }
 
 // The longest cluster's time under the kernel's tile order, in chunks of a
-// 256-wide tile. A chunk costs what its two operand boxes cost the TMA unit (120
-// cycles each, and 64 bytes a cycle): 1260 cycles with 256 columns (32 + 32 KB),
-// 1010 with 128 (32 + 16 KB), 880 with 64 (32 + 8 KB). A tile also costs about a
-// chunk of pipeline fill.
+// 256-wide tile. A chunk is weighed by what its two operand boxes cost one SM's TMA
+// unit (120 cycles each, and 64 bytes a cycle): 1260 cycles with 256 columns (32 + 32
+// KB), 1010 with 128 (32 + 16 KB), 880 with 64 (32 + 8 KB). With all SMs busy a chunk
+// takes longer (1980 with 256), about in proportion to its bytes; the weights serve to
+// choose a width where few tiles are spread badly. A tile also costs about a chunk of
+// pipeline fill.
 double ns_makespan(const NsGemm* g, int count, int bn, int clusters) {
   const double chunk = bn == 256 ? 1.0 : bn == 128 ? 0.8 : 0.7;
   int64_t total = 0;

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(V * R == 1 ? 1024 : 512)
 // ---------------------------------------------------------------- forward, column-wise
 // y of a 128 x 64 tile of h, from the rows' rstd, to column-wise codes. A block does
 // one tile and four blocks share an SM: a tile is a chain of loads and barriers, and
-// the other blocks work meanwhile. (16384 x 2048, both passes: 58.4 us. When it was
+// the other blocks work meanwhile. (16384 x 2048, both passes: 59.2 us. When it was
 // 61, steps of one 512-thread block per SM over 128 x 128 tiles with a TMA ring took
 // 63 and persistent blocks that copy the next tile ahead 66.)
 struct NormColArgs {

@@ -191,7 +191,7 @@ struct GluTileArgs {
 };
 
 // Forward: two tiles per step, half the columns apart, so that the barriers of a
-// step stand beside twice the work (16384 x 6144: 110 us, 5.6 TB/s; one
+// step stand beside twice the work (16384 x 6144: 111 us, 5.5 TB/s; one
 // tile per step, in two blocks per SM, took 6% longer).
 constexpr int kGluFwdSlots = 6;
 using GluFwdRing = TileRing<4, kGluFwdSlots>;      // gate, up, twice
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // Backward, f a multiple of 128 (so that the groups of d do not straddle its
 // two halves): gate, up and da tiles in, a dgate and a dup tile out (16384 x 6144:
-// 170 us, 6.0 TB/s).
+// 171 us, 6.0 TB/s).
 constexpr int kGluBwdSlots = 6;
 using GluBwdRing = TileRing<3, kGluBwdSlots>;
 struct GluBwdSmem {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // is enough. Two pieces come from plain loads: what the block's first step would
 // have been left by the one before it, and in tile m the first dup columns, which
 // share it with the end of dgate.
-// (16384 x 6128: 209 us; 214 with one run per block, for then the blocks are all
+// (16384 x 6128: 216 us. When it was 209: 214 with one run per block, for then the blocks are all
 // over the tensor; 217 with the values shuffled into place instead of other columns
 // per lane; 217 with the pieces of a run's start copied ahead, for the registers;
 // 338 with the kernel below.)

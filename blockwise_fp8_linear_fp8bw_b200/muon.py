@@ -9,8 +9,10 @@ hyperball projection to the initial Frobenius radius, weight decay 0).
 
 The orthogonalisations of all weights run in batched launches (up to eight
 matrices each). A weight's gradient is its fp32 `main_grad` if it has one (as the
-linears of this library accumulate it), else its `.grad`. Momentum, the
-master copy of a bf16 weight and the update are fp32.
+linears of this library accumulate it), else its `.grad`; `zero_grad()` clears the
+latter only, a main_grad is its owner's to clear. Momentum, the master copy of a
+bf16 weight and the update are fp32. A weight whose initial norm is 0 stays 0 under
+the projection.
 """
 import torch
 
