@@ -94,6 +94,12 @@ def _check_norm(x, gamma, r, eps, pow2, rows):
     _padding_is_zero(out, rows)
     y, _, _ = ops.rmsnorm(x, gamma, r, eps)
     assert bool(((y.double() - v).abs() <= err + 2.0 ** -8 * v.abs() + 2.0 ** -134).all())
+    # all outputs of one call are what the calls for each of them give
+    both, every = torch.empty_like(y), [torch.empty_like(t) for t in (*out[:4], out.rstd)]
+    ops.fp8bw_rmsnorm_quantize(x, gamma, r, eps, None if r is None else torch.empty_like(x),
+                               every[4], both, *every[:4], pow2=pow2)
+    assert torch.equal(both, y)
+    assert all(torch.equal(a, b) for a, b in zip(every, (*out[:4], out.rstd)))
     ops.fp8bw_check_device_error()
     return out
 
